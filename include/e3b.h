@@ -323,6 +323,101 @@ E3_API e3_status e3_radial_weights(int64_t E, const float* edge_vec, double cuto
                                    int32_t envelope_p, int32_t hidden, const float* w1, const void* prep,
                                    int32_t n_out, float* w, void* stream);
 
+/* ---------------------------------------------------------------- feature rows --- */
+
+/* Operators on feature rows between two convolutions: rows [N, dim] of irreps blocks in the mul_ir
+ * layout [IRR], any multiplicities and degrees (at most 32 blocks and 2^20 columns).
+ *
+ *   irreps   e.g. "64x0e+64x1o+64x2e";
+ *   groups   number of groups into which every block's channels are cut (group norm only; every
+ *            multiplicity must be divisible by it);
+ *   dtype    of the rows, weights and biases.
+ * A features handle holds no device memory; it is bound to the device current at its creation. */
+typedef struct e3_features e3_features;
+E3_API e3_status e3_features_create(const char* irreps, int32_t groups, e3_dtype dtype, e3_features** features);
+E3_API e3_status e3_features_destroy(e3_features* features);
+/* Columns of a row, channels (copies of an irrep: one weight each), even scalars (0e channels: one
+ * bias each), groups of all blocks together.  Any output pointer may be NULL. */
+E3_API e3_status e3_features_info(const e3_features* features, int64_t* dim, int64_t* n_channels,
+                                  int64_t* n_scalars, int64_t* n_groups);
+
+/* Dropout of whole channels: the 2l+1 components of a channel stay or go together (a mask per
+ * component would not commute with rotations).  Channel u of block b in row i stays iff
+ *   word[u % 4] >= floor(p 2^32),  word = Philox4x32-10(counter = (u / 4, row0 + i, b, offset), key = seed)
+ * (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy as 1, 2, 3", SC 2011), and is then
+ * scaled by 1 / (1 - p).  The mask is a function of these numbers alone: it is never stored, the
+ * backward computes it again, and a rank that holds rows row0 .. row0 + N - 1 of a larger array
+ * drops what a single call on the whole array would drop.
+ *   p       in [0, 1);  offset < 2^32: a call's number (layer, step);
+ *   state   NULL, or a device pointer to {seed, offset} (int64), read by the kernels instead of
+ *           `seed` and `offset`: a captured program draws another mask on each replay if it
+ *           changes them in between.  The backward needs the values its forward saw. */
+typedef struct {
+  double p;
+  uint64_t seed, offset;
+  const int64_t* state;
+  int64_t row0;
+} e3_dropout_spec;
+
+/* out = dropout(x) (+ residual if not NULL), all [N, dim]; a dropped channel gives 0 whatever its
+ * value.  out may be x or residual.  It is its own backward: grad_x = dropout(grad_out) with the
+ * same drop.  N == 0 is a no-op. */
+E3_API e3_status e3_dropout(const e3_features* features, int64_t N, const void* x, const void* residual,
+                            const e3_dropout_spec* drop, void* out, void* stream);
+
+/* Activation of the even scalars (other irreps pass unchanged: a pointwise function of a component
+ * does not commute with rotations). */
+typedef enum { E3_ACT_NONE = 0, E3_ACT_SILU = 1 } e3_act;
+
+/* Group norm with an activation and dropout.  The rows are cut into B segments (the structures of a
+ * batch), segment s holding rows row_ptr[s] .. row_ptr[s+1] - 1; statistics are taken over the n
+ * values of a (segment, group) pair: all rows of the segment, all components of the group's channels.
+ *   mu = mean(x) for even scalars (0e), 0 for every other irrep,
+ *   r = (mean((x - mu)^2) + eps)^(-1/2),   z = (x - mu) r,
+ *   t = weight[channel] z + bias[channel]      (bias: 0e channels only),
+ *   y = dropout(act(t)).
+ * Arguments:
+ *   row_ptr  device int32 [B + 1], row_ptr[0] == 0, non-decreasing, row_ptr[B] <= N; NULL with B == 1:
+ *            one segment of all N rows.  Rows from row_ptr[B] on are padding: never read, zero in
+ *            every output row.  Segments may be empty.  Other pointers record E3_ERR_INDEX (the
+ *            rows touched stay inside [0, N); results are then unspecified).
+ *   max_rows a hint that selects the kernels: an upper bound on the rows of a segment, or 0 if
+ *            unknown.  Results are right for any value.
+ *   weight   [n_channels] or NULL (ones); bias [n_scalars] or NULL (zeros);
+ *   drop     NULL: none;
+ *   stats    device [B, n_groups, 2] doubles: (mu, r), written by the forward, read by the backward;
+ *   workspace  device buffer of e3_group_norm_workspace_size bytes, 16-byte aligned, not used by any
+ *            other call while this one runs on its stream.
+ * Sums run in the rows' type over at most 64 rows and in double from there on, in a fixed order:
+ * results are bitwise repeatable.  N < 2^31, 1 <= B < 2^31.  N == 0 leaves every row output alone and
+ * zero-fills the parameters' gradients. */
+E3_API e3_status e3_group_norm_workspace_size(const e3_features* features, int64_t N, int64_t B, int64_t max_rows,
+                                              size_t* bytes);
+E3_API e3_status e3_group_norm_forward(const e3_features* features, int64_t N, int64_t B, const int32_t* row_ptr,
+                                       int64_t max_rows, const void* x, const void* weight, const void* bias,
+                                       double eps, e3_act act, const e3_dropout_spec* drop, void* y, double* stats,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of <grad_y, y>: with h = grad_y dropout' act'(t), c = weight h,
+ *   grad_x = r (c - [0e] mean(c) - z mean(c z)), grad_weight = sum h z, grad_bias = sum h.
+ * Each output may be NULL to skip it; outputs are overwritten.  Other arguments as the forward's. */
+E3_API e3_status e3_group_norm_backward(const e3_features* features, int64_t N, int64_t B, const int32_t* row_ptr,
+                                        int64_t max_rows, const void* x, const double* stats, const void* weight,
+                                        const void* bias, e3_act act, const e3_dropout_spec* drop,
+                                        const void* grad_y, void* grad_x, void* grad_weight, void* grad_bias,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* The backward of e3_group_norm_backward (force training differentiates the forces): gradients of
+ * <u_x, grad_x> + <u_weight, grad_weight> + <u_bias, grad_bias> with respect to grad_y, x, weight and
+ * bias.  u_x [N, dim], u_weight, u_bias: each may be NULL (zero).  Each output may be NULL to skip it. */
+E3_API e3_status e3_group_norm_double_backward(const e3_features* features, int64_t N, int64_t B,
+                                               const int32_t* row_ptr, int64_t max_rows, const void* x,
+                                               const double* stats, const void* weight, const void* bias, e3_act act,
+                                               const e3_dropout_spec* drop, const void* grad_y, const void* u_x,
+                                               const void* u_weight, const void* u_bias, void* d_grad_y, void* d_x,
+                                               void* d_weight, void* d_bias, void* workspace,
+                                               size_t workspace_bytes, void* stream);
+
 /* ----------------------------------------------------------------------- convolution --- */
 
 /* Work units of the convolution for one topology [CONV]: each receiver's in-edges (receiver CSR)

@@ -38,11 +38,7 @@ void clear_error() { g_last_error.clear(); }
 // ------------------------------------------------------------------ irreps strings ---
 // e3nn course, "Curriculum at a glance", lesson 02a: terms "<mul>x<l><p>" joined by '+';
 // a bare "<l><p>" has multiplicity 1.
-struct IrrepT {
-  int mul, l, p;
-};
-
-static bool parse_irreps(const char* s, std::vector<IrrepT>* out, std::string* why) {
+bool parse_irreps(const char* s, std::vector<IrrepT>* out, std::string* why) {
   out->clear();
   if (s == nullptr) {
     *why = "NULL irreps string";

@@ -19,6 +19,7 @@ STATUS_NAMES = ["OK", "INVALID_ARG", "IRREPS_PARSE", "INSTRUCTION", "UNSUPPORTED
                 "CUDA", "TIMEOUT"]
 _DTYPES = {torch.float32: 0, torch.float64: 1}
 _SH_NORMS = {"component": 0, "integral": 1, "norm": 2}
+_ACTS = {None: 0, "silu": 1}
 
 # every symbol include/e3b.h declares
 SYMBOLS = [
@@ -30,7 +31,9 @@ SYMBOLS = [
     "e3_morton_order", "e3_invert_permutation", "e3_remap_ids", "e3_conv_workspace_size",
     "e3_conv_topology_size", "e3_conv_topology_build", "e3_set_test_knobs", "e3_add_rows",
     "e3_conv_topology_build_ordered", "e3_radial_prep_size", "e3_radial_prepare", "e3_radial_weights",
-    "e3_spherical_harmonics_double_backward", "e3_plan_status",
+    "e3_spherical_harmonics_double_backward", "e3_plan_status", "e3_features_create", "e3_features_destroy",
+    "e3_features_info", "e3_dropout", "e3_group_norm_workspace_size", "e3_group_norm_forward",
+    "e3_group_norm_backward", "e3_group_norm_double_backward",
 ]
 
 
@@ -44,6 +47,11 @@ class E3Error(RuntimeError):
 class Instruction(ctypes.Structure):
     _fields_ = [("i_in1", ctypes.c_int32), ("i_in2", ctypes.c_int32), ("i_out", ctypes.c_int32),
                 ("has_weight", ctypes.c_int32), ("path_weight", ctypes.c_double)]
+
+
+class DropoutSpec(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("state", ctypes.c_void_p), ("row0", ctypes.c_int64)]
 
 
 def _load():
@@ -91,6 +99,18 @@ def _load():
         "e3_invert_permutation": [I64, VP, VP, VP],
         "e3_remap_ids": [I64, VP, I64, VP, VP, VP],
         "e3_set_test_knobs": [I64, I32],
+        "e3_features_create": [P, I32, ctypes.c_int, ctypes.POINTER(VP)],
+        "e3_features_destroy": [VP],
+        "e3_features_info": [VP, ctypes.POINTER(I64), ctypes.POINTER(I64), ctypes.POINTER(I64), ctypes.POINTER(I64)],
+        "e3_dropout": [VP, I64, VP, VP, ctypes.POINTER(DropoutSpec), VP, VP],
+        "e3_group_norm_workspace_size": [VP, I64, I64, I64, ctypes.POINTER(ctypes.c_size_t)],
+        "e3_group_norm_forward": [VP, I64, I64, VP, I64, VP, VP, VP, D, ctypes.c_int, ctypes.POINTER(DropoutSpec), VP,
+                                  VP, VP, ctypes.c_size_t, VP],
+        "e3_group_norm_backward": [VP, I64, I64, VP, I64, VP, VP, VP, VP, ctypes.c_int, ctypes.POINTER(DropoutSpec),
+                                   VP, VP, VP, VP, VP, ctypes.c_size_t, VP],
+        "e3_group_norm_double_backward": [VP, I64, I64, VP, I64, VP, VP, VP, VP, ctypes.c_int,
+                                          ctypes.POINTER(DropoutSpec), VP, VP, VP, VP, VP, VP, VP, VP, VP,
+                                          ctypes.c_size_t, VP],
         "e3_last_error": [],
     }
     for name, args in sig.items():
@@ -639,3 +659,277 @@ def conv_vec(plan, graph, x, edge_vec, w, out_scale=1.0, sh_norm="component"):
     """Differentiable convolution with harmonics computed in the kernels from edge vectors
     (receiver order): gradients with respect to x, edge_vec (through the harmonics) and w."""
     return _ConvVecFn.apply(x, edge_vec, w, plan, graph, out_scale, sh_norm)
+
+
+class Features:
+    """The layout of feature rows [N, dim] for ``group_norm`` and ``dropout``: an irreps string in the
+    mul_ir layout (any multiplicities and degrees), the number of groups into which every block's
+    channels are cut, and the rows' dtype; bound to the current CUDA device (e3_features_create).
+
+    ``n_channels`` weights (one per copy of an irrep), ``n_scalars`` biases (0e channels only),
+    ``n_groups`` groups over all blocks."""
+
+    def __init__(self, irreps, groups=1, dtype=torch.float32):
+        if dtype not in _DTYPES:
+            raise ValueError("dtype must be torch.float32 or torch.float64")
+        handle = ctypes.c_void_p()
+        self._handle = None
+        _check(lib.e3_features_create(irreps.encode(), int(groups), _DTYPES[dtype], ctypes.byref(handle)))
+        self._handle = handle
+        self.irreps, self.groups, self.dtype = irreps, int(groups), dtype
+        vals = [ctypes.c_int64() for _ in range(4)]
+        _check(lib.e3_features_info(handle, *(ctypes.byref(v) for v in vals)))
+        self.dim, self.n_channels, self.n_scalars, self.n_groups = (v.value for v in vals)
+        self.device = torch.device("cuda", torch.cuda.current_device()) if torch.cuda.is_available() else None
+
+    def __del__(self):
+        if getattr(self, "_handle", None) and lib is not None:
+            try:
+                lib.e3_features_destroy(self._handle)
+            except Exception:  # interpreter shutdown
+                pass
+            self._handle = None
+
+    @property
+    def handle(self):
+        return self._handle
+
+
+class Segments:
+    """Rows of a batch cut into structures: segment s holds rows row_ptr[s] .. row_ptr[s+1] - 1 of
+    ``n_rows``; rows from row_ptr[-1] on are padding.  ``row_ptr``: int32 CUDA tensor [B + 1] starting
+    at 0.  ``max_rows``: an upper bound on a segment's rows if the host knows one (it selects the
+    kernels; results do not depend on it)."""
+
+    def __init__(self, row_ptr, n_rows, max_rows=None):
+        if not isinstance(row_ptr, torch.Tensor) or row_ptr.dim() != 1 or row_ptr.shape[0] < 2:
+            raise ValueError("row_ptr must be a one-dimensional tensor of at least two entries")
+        if row_ptr.device.type != "cuda":
+            raise ValueError("row_ptr must be a CUDA tensor")
+        _need(row_ptr, "row_ptr", torch.int32, row_ptr.shape, row_ptr.device)
+        if n_rows < 0 or (max_rows is not None and max_rows < 0):
+            raise ValueError("n_rows and max_rows must not be negative")
+        self.row_ptr, self.n_rows = row_ptr, int(n_rows)
+        self.n_segments = row_ptr.shape[0] - 1
+        # every segment empty: any positive bound holds
+        self.max_rows = 0 if max_rows is None else max(1, int(max_rows))
+
+    @classmethod
+    def from_counts(cls, counts, n_rows=None, device=None):
+        """From the rows of each segment (host numbers); ``n_rows`` above their sum adds padding rows."""
+        counts = [int(c) for c in counts]
+        if not counts or min(counts) < 0:
+            raise ValueError("counts must be a non-empty list of non-negative numbers")
+        total = sum(counts)
+        n_rows = total if n_rows is None else int(n_rows)
+        if total > n_rows:
+            raise ValueError(f"counts add up to {total} rows of {n_rows}")
+        if n_rows >= 2 ** 31:
+            raise ValueError("n_rows passes 2^31")
+        ptr = torch.zeros(len(counts) + 1, dtype=torch.int32)
+        ptr[1:] = torch.tensor(counts, dtype=torch.int64).cumsum(0)
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+        return cls(ptr.to(device), n_rows, max_rows=max(counts))
+
+
+def _drop_spec(features, p, rng, row0):
+    """The C dropout argument, or None when nothing is dropped."""
+    p = float(p)
+    if not 0.0 <= p < 1.0:
+        raise ValueError(f"p must be in [0, 1), got {p}")
+    if p == 0.0:
+        return None
+    if rng is None:
+        raise ValueError("dropout needs rng: a seed, a (seed, offset) pair or an int64 CUDA tensor [2]")
+    if isinstance(rng, torch.Tensor):
+        _need(rng, "rng", torch.int64, (2,), features.device)
+        return DropoutSpec(p, 0, 0, rng.data_ptr(), int(row0))
+    seed, offset = rng if isinstance(rng, (tuple, list)) else (rng, 0)
+    seed, offset = int(seed), int(offset)
+    if not -2 ** 63 <= seed < 2 ** 64 or not 0 <= offset < 2 ** 32:
+        raise ValueError("the seed must fit 64 bits, the offset 32")
+    return DropoutSpec(p, seed % 2 ** 64, offset, None, int(row0))
+
+
+def dropout_forward(features, x, p, rng, residual=None, row0=0, out=None):
+    """Dropout of whole channels of rows x [N, dim], plus ``residual`` if given (e3_dropout).
+    ``rng``: a seed, a (seed, offset) pair, or an int64 CUDA tensor [seed, offset] read when the kernel
+    runs (for captured programs).  ``row0``: index of the first row in a larger, sharded array.
+    ``out`` may be x or residual.  The mask depends on rng, row and channel only, so the gradient
+    with respect to x is this call on the gradient."""
+    N, dt, dev = x.shape[0], features.dtype, features.device
+    shape = (N, features.dim)
+    _need(x, "x", dt, shape, dev)
+    if residual is not None:
+        _need(residual, "residual", dt, shape, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", dt, shape, dev)
+    spec = _drop_spec(features, p, rng, row0)
+    _check(lib.e3_dropout(features.handle, N, _ptr(x), _ptr(residual), None if spec is None else ctypes.byref(spec),
+                          _ptr(out), _stream()))
+    return out
+
+
+class _DropoutFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, features, p, rng, row0):
+        ctx.features, ctx.p, ctx.row0, ctx.has_residual = features, p, row0, residual is not None
+        ctx.rng = None if isinstance(rng, torch.Tensor) else rng
+        ctx.save_for_backward(*([rng] if isinstance(rng, torch.Tensor) else []))
+        return dropout_forward(features, x, p, rng, residual=residual, row0=row0)
+
+    @staticmethod
+    def backward(ctx, g):
+        rng = ctx.saved_tensors[0] if ctx.saved_tensors else ctx.rng
+        gx = None
+        if ctx.needs_input_grad[0]:
+            gx = _DropoutFn.apply(g.contiguous(), None, ctx.features, ctx.p, rng, ctx.row0)
+        return gx, g if ctx.has_residual else None, None, None, None, None
+
+
+def dropout(features, x, p, rng, residual=None, row0=0):
+    """Differentiable (any order) dropout of whole channels plus an optional residual; see
+    ``dropout_forward``.  An rng tensor must keep its values until the backward has run."""
+    return _DropoutFn.apply(x, residual, features, p, rng, row0)
+
+
+def _norm_args(features, x, weight, bias, segments, act):
+    N, dt, dev = x.shape[0], features.dtype, features.device
+    _need(x, "x", dt, (N, features.dim), dev)
+    if weight is not None:
+        _need(weight, "weight", dt, (features.n_channels,), dev)
+    if bias is not None:
+        _need(bias, "bias", dt, (features.n_scalars,), dev)
+    if act not in _ACTS:
+        raise ValueError(f"act must be None or 'silu', got {act!r}")
+    if segments is None:
+        return N, 1, None, N
+    if segments.n_rows != N:
+        raise ValueError(f"x has {N} rows, the segments were made for {segments.n_rows}")
+    if segments.row_ptr.device != dev:
+        raise ValueError(f"segments are on {segments.row_ptr.device}, expected {dev}")
+    return N, segments.n_segments, segments.row_ptr, segments.max_rows
+
+
+def _norm_workspace(features, N, B, max_rows):
+    nbytes = ctypes.c_size_t()
+    _check(lib.e3_group_norm_workspace_size(features.handle, N, B, max_rows, ctypes.byref(nbytes)))
+    return torch.empty(nbytes.value, dtype=torch.uint8, device=features.device)
+
+
+def group_norm_forward(features, x, weight=None, bias=None, segments=None, eps=1e-5, act=None, p=0.0, rng=None,
+                       row0=0, out=None):
+    """(y, stats): group norm of rows x [N, dim] over the segments (None: one segment of all rows), then
+    the activation on the 0e channels, then dropout (e3_group_norm_forward).  ``stats`` [B, n_groups, 2]
+    float64 holds (mean, 1 / deviation) for the backward.  Padding rows of y are zero."""
+    N, B, row_ptr, max_rows = _norm_args(features, x, weight, bias, segments, act)
+    spec = _drop_spec(features, p, rng, row0)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", features.dtype, x.shape, features.device)
+    stats = torch.empty((B, features.n_groups, 2), dtype=torch.float64, device=features.device)
+    ws = _norm_workspace(features, N, B, max_rows)
+    _check(lib.e3_group_norm_forward(features.handle, N, B, _ptr(row_ptr), max_rows, _ptr(x), _ptr(weight), _ptr(bias),
+                                     float(eps), _ACTS[act], None if spec is None else ctypes.byref(spec), _ptr(out),
+                                     _ptr(stats), _ptr(ws), ws.numel(), _stream()))
+    return out, stats
+
+
+def group_norm_backward(features, x, stats, grad_y, weight=None, bias=None, segments=None, act=None, p=0.0, rng=None,
+                        row0=0, need_x=True, need_weight=True, need_bias=True):
+    """(grad_x, grad_weight, grad_bias) of <grad_y, y> (e3_group_norm_backward); skipped ones are None.
+    Arguments as the forward's, with its ``stats``."""
+    N, B, row_ptr, max_rows = _norm_args(features, x, weight, bias, segments, act)
+    dt, dev = features.dtype, features.device
+    _need(stats, "stats", torch.float64, (B, features.n_groups, 2), dev)
+    _need(grad_y, "grad_y", dt, x.shape, dev)
+    spec = _drop_spec(features, p, rng, row0)
+    gx = torch.empty_like(x) if need_x else None
+    gw = torch.empty(features.n_channels, dtype=dt, device=dev) if need_weight else None
+    gb = torch.empty(features.n_scalars, dtype=dt, device=dev) if need_bias else None
+    ws = _norm_workspace(features, N, B, max_rows)
+    _check(lib.e3_group_norm_backward(features.handle, N, B, _ptr(row_ptr), max_rows, _ptr(x), _ptr(stats),
+                                      _ptr(weight), _ptr(bias), _ACTS[act],
+                                      None if spec is None else ctypes.byref(spec), _ptr(grad_y), _ptr(gx), _ptr(gw),
+                                      _ptr(gb), _ptr(ws), ws.numel(), _stream()))
+    return gx, gw, gb
+
+
+def group_norm_double_backward(features, x, stats, grad_y, weight=None, bias=None, u_x=None, u_weight=None,
+                               u_bias=None, segments=None, act=None, p=0.0, rng=None, row0=0, need_grad_y=True,
+                               need_x=True, need_weight=True, need_bias=True):
+    """(d_grad_y, d_x, d_weight, d_bias): the backward of ``group_norm_backward`` for upstream gradients
+    u_x, u_weight, u_bias of its three results, None being zero (e3_group_norm_double_backward)."""
+    N, B, row_ptr, max_rows = _norm_args(features, x, weight, bias, segments, act)
+    dt, dev = features.dtype, features.device
+    _need(stats, "stats", torch.float64, (B, features.n_groups, 2), dev)
+    _need(grad_y, "grad_y", dt, x.shape, dev)
+    for t, name, shape in ((u_x, "u_x", x.shape), (u_weight, "u_weight", (features.n_channels,)),
+                           (u_bias, "u_bias", (features.n_scalars,))):
+        if t is not None:
+            _need(t, name, dt, shape, dev)
+    spec = _drop_spec(features, p, rng, row0)
+    dg = torch.empty_like(x) if need_grad_y else None
+    dx = torch.empty_like(x) if need_x else None
+    dw = torch.empty(features.n_channels, dtype=dt, device=dev) if need_weight else None
+    db = torch.empty(features.n_scalars, dtype=dt, device=dev) if need_bias else None
+    ws = _norm_workspace(features, N, B, max_rows)
+    _check(lib.e3_group_norm_double_backward(features.handle, N, B, _ptr(row_ptr), max_rows, _ptr(x), _ptr(stats),
+                                             _ptr(weight), _ptr(bias), _ACTS[act],
+                                             None if spec is None else ctypes.byref(spec), _ptr(grad_y), _ptr(u_x),
+                                             _ptr(u_weight), _ptr(u_bias), _ptr(dg), _ptr(dx), _ptr(dw), _ptr(db),
+                                             _ptr(ws), ws.numel(), _stream()))
+    return dg, dx, dw, db
+
+
+def _contiguous(t):
+    return None if t is None else t.contiguous()
+
+
+class _NormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, features, segments, eps, act, p, rng, row0):
+        ctx.features, ctx.rng = features, rng
+        ctx.kw = dict(segments=segments, act=act, p=p, row0=row0)
+        y, stats = group_norm_forward(features, x, weight, bias, eps=eps, rng=rng, **ctx.kw)
+        ctx.save_for_backward(x, weight, bias, stats, rng if isinstance(rng, torch.Tensor) else None)
+        return y
+
+    @staticmethod
+    def backward(ctx, g):
+        x, weight, bias, stats, rng = ctx.saved_tensors
+        gx, gw, gb = _NormBwdFn.apply(x, weight, bias, g.contiguous(), stats, ctx.features,
+                                      ctx.rng if rng is None else rng, tuple(ctx.needs_input_grad[:3]), ctx.kw)
+        return gx, gw, gb, None, None, None, None, None, None, None
+
+
+class _NormBwdFn(torch.autograd.Function):
+    """The group norm's backward as a differentiable function of (x, weight, bias, grad_y)."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, g, stats, features, rng, needs, kw):
+        ctx.features, ctx.rng, ctx.kw = features, rng, kw
+        ctx.save_for_backward(x, weight, bias, g, stats, rng if isinstance(rng, torch.Tensor) else None)
+        ctx.set_materialize_grads(False)
+        return group_norm_backward(features, x, stats, g, weight, bias, rng=rng, need_x=needs[0],
+                                   need_weight=needs[1], need_bias=needs[2], **kw)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, ux, uw, ub):
+        x, weight, bias, g, stats, rng = ctx.saved_tensors
+        nx, nw, nb, ng = ctx.needs_input_grad[:4]
+        dg, dx, dw, db = group_norm_double_backward(
+            ctx.features, x, stats, g, weight, bias, u_x=_contiguous(ux), u_weight=_contiguous(uw),
+            u_bias=_contiguous(ub), rng=ctx.rng if rng is None else rng, need_grad_y=ng, need_x=nx, need_weight=nw,
+            need_bias=nb, **ctx.kw)
+        return dx, dw, db, dg, None, None, None, None, None
+
+
+def group_norm(features, x, weight=None, bias=None, segments=None, eps=1e-5, act=None, p=0.0, rng=None, row0=0):
+    """Twice-differentiable group norm with activation and dropout (x, weight, bias; see
+    ``group_norm_forward``).  An rng tensor must keep its values until the backward has run."""
+    return _NormFn.apply(x, weight, bias, features, segments, eps, act, p, rng, row0)

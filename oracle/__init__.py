@@ -13,7 +13,9 @@ what the method computes, written from the mathematics the sources state and not
 * the point convolution with receiver aggregation (lesson 06a; E3J summary, section E.2.2);
 * reverse mode by transposition of the multilinear map (E3J summary, section E.1);
 * the radial network (Bessel basis, polynomial envelope, SiLU MLP) that gives the per-edge path
-  weights (lessons 05b and 06a).
+  weights (lessons 05b and 06a);
+* the operators on feature rows between convolutions: group norm with an activation, its first and
+  second derivatives, and counter-based dropout of whole channels.
 
 Only ``tests/``, ``__graft_entry__.smoke()`` and the ``cpu_baseline`` / ``--impl reference``
 legs of ``bench.py`` may import it.  It shares no code with the CUDA library and must never
@@ -26,6 +28,8 @@ from .cg import complex_cg, real_cg, real_basis_change
 from .tp import Instruction, TPPlan, make_plan, tp_forward, tp_backward
 from .conv import csr_build, conv_forward, conv_backward
 from .reorder import morton_codes, morton_order, invert_permutation
+from .features import (philox4x32, dropout_keep, dropout_factor, group_norm, group_norm_backward,
+                       group_norm_double_backward)
 from .radial import bessel_basis, polynomial_envelope, silu, radial_weights
 
 __all__ = [
@@ -34,4 +38,5 @@ __all__ = [
     "real_basis_change", "Instruction", "TPPlan", "make_plan", "tp_forward", "tp_backward",
     "csr_build", "conv_forward", "conv_backward", "morton_codes", "morton_order", "invert_permutation",
     "bessel_basis", "polynomial_envelope", "silu", "radial_weights",
+    "philox4x32", "dropout_keep", "dropout_factor", "group_norm", "group_norm_backward", "group_norm_double_backward",
 ]
