@@ -326,7 +326,7 @@ E3_API e3_status e3_radial_weights(int64_t E, const float* edge_vec, double cuto
 /* ---------------------------------------------------------------- feature rows --- */
 
 /* Operators on feature rows between two convolutions: rows [N, dim] of irreps blocks in the mul_ir
- * layout [IRR], any multiplicities and degrees (at most 32 blocks and 2^20 columns).
+ * layout [IRR], any multiplicities, degrees up to 127 (at most 32 blocks and 32768 columns).
  *
  *   irreps   e.g. "64x0e+64x1o+64x2e";
  *   groups   number of groups into which every block's channels are cut (group norm only; every
@@ -381,15 +381,16 @@ typedef enum { E3_ACT_NONE = 0, E3_ACT_SILU = 1 } e3_act;
  *            one segment of all N rows.  Rows from row_ptr[B] on are padding: never read, zero in
  *            every output row.  Segments may be empty.  Other pointers record E3_ERR_INDEX (the
  *            rows touched stay inside [0, N); results are then unspecified).
- *   max_rows a hint that selects the kernels: an upper bound on the rows of a segment, or 0 if
- *            unknown.  Results are right for any value.
+ *   max_rows an upper bound on the rows of a segment, or 0 if unknown; it selects the kernels.  A segment
+ *            that is longer records E3_ERR_INDEX where its surplus rows find no place (they are skipped).
  *   weight   [n_channels] or NULL (ones); bias [n_scalars] or NULL (zeros);
  *   drop     NULL: none;
- *   stats    device [B, n_groups, 2] doubles: (mu, r), written by the forward, read by the backward;
+ *   stats    device [B, n_groups, 2] doubles: (mu, r), written by the forward (unspecified for an empty
+ *            segment), read by the backward;
  *   workspace  device buffer of e3_group_norm_workspace_size bytes, 16-byte aligned, not used by any
  *            other call while this one runs on its stream.
- * Sums run in the rows' type over at most 64 rows and in double from there on, in a fixed order:
- * results are bitwise repeatable.  N < 2^31, 1 <= B < 2^31.  N == 0 leaves every row output alone and
+ * Sums run in the rows' type over at most 64 rows of a thread, and over a segment that fits one block
+ * of threads; in double from there on.  Their order is fixed: results are bitwise repeatable.  N < 2^31, 1 <= B < 2^31.  N == 0 leaves every row output alone and
  * zero-fills the parameters' gradients. */
 E3_API e3_status e3_group_norm_workspace_size(const e3_features* features, int64_t N, int64_t B, int64_t max_rows,
                                               size_t* bytes);

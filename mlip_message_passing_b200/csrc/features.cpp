@@ -29,6 +29,7 @@ extern "C" e3_status e3_features_create(const char* irreps, int32_t groups, e3_d
   RowLayout& L = f->lay;
   L.n_blocks = int32_t(ir.size());
   L.groups = groups;
+  L.div_groups = reciprocal(uint32_t(groups));
   for (size_t i = 0; i < ir.size(); ++i) {
     const IrrepT& t = ir[i];
     if (t.l > FR_MAX_L) return fail(E3_ERR_UNSUPPORTED, "degree %d is above %d", t.l, FR_MAX_L);
@@ -44,11 +45,14 @@ extern "C" e3_status e3_features_create(const char* irreps, int32_t groups, e3_d
     col += int64_t(t.mul) * b.d;
     if (col > FR_MAX_DIM) return fail(E3_ERR_UNSUPPORTED, "rows of more than %lld columns", (long long)FR_MAX_DIM);
     b.group_cols = t.mul / groups * b.d;
+    b.div_d = reciprocal(uint32_t(b.d));
+    b.div_group = reciprocal(uint32_t(b.group_cols));
     L.n_channels += t.mul;
     if (scalar) L.n_scalars += t.mul;
   }
   L.dim = int32_t(col);
   f->dtype = dtype;
+  make_tiles(f.get());
   // without a device the layout can still be described (host checks); the calls refuse it
   if (cudaGetDevice(&f->device) != cudaSuccess) {
     cudaGetLastError();

@@ -2,14 +2,20 @@
 #pragma once
 
 #include <cstdint>
+#include <vector>
 
 #include "../../include/e3b.h"
+
+#ifndef __CUDACC__
+#define __host__
+#define __device__
+#endif
 
 namespace e3b {
 
 constexpr int FR_MAXB = 32;             // irrep blocks at most
-constexpr int FR_MAX_L = 500;            // degree of a block at most
-constexpr int64_t FR_MAX_DIM = 1 << 20;  // columns of a row at most
+constexpr int FR_MAX_L = 127;           // degree of a block at most
+constexpr int64_t FR_MAX_DIM = 32768;   // columns of a row at most
 
 struct RowBlock {
   int32_t col0;        // first column
@@ -17,12 +23,16 @@ struct RowBlock {
   int32_t group_cols;  // columns of one group: mul / groups * d
   int32_t chan0;       // index of its first channel among all channels
   int32_t bias0;       // index of its first channel among the even scalars, -1 for other irreps
+  uint32_t div_d, div_group;  // reciprocals of d and group_cols (fast_div)
 };
+// x / n = umulhi(x, reciprocal(n)) for 1 < n and x n < 2^32; 0 stands for n = 1.
+inline uint32_t reciprocal(uint32_t n) { return n > 1 ? uint32_t(0xFFFFFFFFu / n) + 1u : 0u; }
 
 struct RowLayout {
   int32_t n_blocks, groups, dim, n_channels, n_scalars;
+  uint32_t div_groups;
   RowBlock blk[FR_MAXB];
-  int32_t n_groups() const { return n_blocks * groups; }
+  __host__ __device__ int32_t n_groups() const { return n_blocks * groups; }
 };
 
 // Dropout as the kernels take it: a channel stays when its word is >= thr.
@@ -36,8 +46,19 @@ struct DropArgs {
 
 // Validate `drop` (NULL: no dropout) for N rows; *on tells whether anything is dropped.
 e3_status drop_args(const e3_dropout_spec* drop, int64_t N, DropArgs* out, bool* on);
+// Tiles of the group norm (group_norm.cu), once per features.
+void make_tiles(e3_features* f);
 // f is not NULL and its device is current.
 e3_status check_features_device(const e3_features* f);
+
+// A cut of a row's vector columns into tiles of at most tx: whole groups, or parts of one group that is
+// wider than a block of threads (`cut`).
+struct TileSet {
+  int tx = 0;
+  bool cut = false;
+  std::vector<int32_t> first;  // first vector column of each tile, then the end
+  int n() const { return int(first.size()) - 1; }
+};
 
 }  // namespace e3b
 
@@ -45,4 +66,8 @@ struct e3_features {
   int device = 0;
   e3_dtype dtype = E3_F32;
   e3b::RowLayout lay{};
+  int vec = 1;                   // group norm: columns of a vector
+  bool cluster_ok = false;       // group norm: the tiles for long segments suit clusters
+  int wide = 0;                  // widest group in vectors
+  e3b::TileSet local[9], grid;   // tiles for 2^i row lanes of a segment; for long segments
 };

@@ -8,145 +8,113 @@ namespace {
 
 size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 
-// 16-byte vectors need every group to be a whole number of them (then every block, and the row, is).
-int vec_of(const RowLayout& L, e3_dtype dt) {
-  const int v = dt == E3_F64 ? 2 : 4;
-  for (int b = 0; b < L.n_blocks; ++b)
-    if (L.blk[b].group_cols % v != 0) return 1;
-  return v;
-}
-
-int pow2_at_least(int64_t n) {
-  int p = 1;
-  while (p < n && p < 32) p *= 2;
-  return p;
-}
-
-GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows, int op, NormArgs* a) {
-  const RowLayout& L = f->lay;
-  GnConfig c;
-  c.vec = vec_of(L, f->dtype);
-  const int V = L.dim / c.vec;
-  int wide = 0;  // widest group in vectors
-  for (int b = 0; b < L.n_blocks; ++b) wide = std::max(wide, L.blk[b].group_cols / c.vec);
-  const int64_t most = max_rows > 0 ? std::min(max_rows, N) : N;
-  const int RP = gn_reg_rows(op);
-  // local: a segment's widest group fits the registers of one CTA
-  if (wide <= GN_THREADS && most <= int64_t(RP) * (GN_THREADS / wide)) {
-    int K = int(std::max<int64_t>(1, (most + RP - 1) / RP));
-    const int cap = std::max(wide, GN_THREADS / K);
-    a->n_slabs = 0;
-    a->slab[0] = 0;
-    int tx = 0, at = 0;
-    bool fits = true;
-    for (int b = 0; b < L.n_blocks && fits; ++b)
-      for (int g = 0; g < L.groups; ++g) {
-        const int w = L.blk[b].group_cols / c.vec;
-        if (at + w - a->slab[a->n_slabs] > cap) {
-          if (a->n_slabs + 2 > GN_MAXSLAB) {
-            fits = false;
-            break;
-          }
-          a->slab[++a->n_slabs] = at;
-        }
+// Cut the row into tiles of at most `cap` vectors: groups in order, as many as fit; a group wider than
+// cap is cut at whole channels (a channel is d columns; a vector holds parts of whole quads).
+TileSet cut_tiles(const RowLayout& L, int vec, int cap) {
+  TileSet t;
+  t.first.push_back(0);
+  int at = 0;
+  for (int b = 0; b < L.n_blocks; ++b) {
+    const int w = L.blk[b].group_cols / vec, d = L.blk[b].d;
+    for (int g = 0; g < L.groups; ++g) {
+      if (at + w - t.first.back() > cap && at > t.first.back()) t.first.push_back(at);
+      if (w > cap) {
+        const int step = std::max(1, cap / d) * d;
+        for (int o = step; o < w; o += step) t.first.push_back(at + o);
+        t.cut = true;
         at += w;
-        tx = std::max(tx, at - a->slab[a->n_slabs]);
+        t.first.push_back(at);
+      } else {
+        at += w;
       }
-    if (fits) {
-      a->slab[++a->n_slabs] = at;
-      c.local = true;
-      a->tx = tx;
-      a->j = std::max(1, GN_THREADS / (tx * K));
-      a->k = a->j == 1 ? std::max(K, GN_THREADS / tx) : K;
-      a->lanes = pow2_at_least(int64_t(a->k) * wide);
-      const int64_t batches = (B + a->j - 1) / a->j;
-      const int64_t want = std::max<int64_t>(1, int64_t(8) * sm_count() / a->n_slabs);
-      c.grid = dim3(unsigned(std::min(batches, want)), unsigned(a->n_slabs));
-      c.col_parts = c.grid.x;
     }
   }
-  size_t at = 0;
-  if (!c.local) {
-    a->tx = std::min(V, 64);
-    a->k = GN_THREADS / a->tx;
-    a->j = 1;
-    a->n_tiles = (V + a->tx - 1) / a->tx;
-    a->lanes = pow2_at_least(int64_t(a->k) * std::min(wide, a->tx));
-    const int64_t want = std::max<int64_t>(1, int64_t(4) * sm_count() / a->n_tiles);
-    const int64_t least = int64_t(a->k) * 8;
-    a->rows_cta = std::max((N + want - 1) / want, least);
-    a->n_chunks = (N + a->rows_cta - 1) / a->rows_cta;
-    c.grid = dim3(unsigned(a->n_chunks), unsigned(a->n_tiles));
-    c.col_parts = a->n_chunks;
-    const size_t G = size_t(L.n_groups());
-    c.part = 0;
-    c.coef = al256(size_t(a->n_chunks + B) * (G + size_t(a->n_tiles)) * gn_sums(op) * 8);
-    at = c.coef + al256(size_t(B) * G * gn_coefs(op) * 8);
+  if (t.first.back() != at) t.first.push_back(at);
+  for (int i = 0; i + 1 < int(t.first.size()); ++i) t.tx = std::max(t.tx, t.first[i + 1] - t.first[i]);
+  return t;
+}
+
+// The cut between `lo` and `hi` that leaves the fewest of a block's threads idle (the narrowest of equals).
+TileSet best_tiles(const RowLayout& L, int vec, int lo, int hi, int k) {
+  TileSet best;
+  double score = -1.0;
+  const int V = L.dim / vec;
+  for (int cap = lo; cap <= hi; ++cap) {
+    TileSet t = cut_tiles(L, vec, cap);
+    if (t.n() > GN_MAXTILE) continue;
+    const int lanes = k > 0 ? k * std::max(1, GN_THREADS / (t.tx * k)) : GN_THREADS / t.tx;
+    const double u = double(V) / (double(t.n()) * t.tx) * (double(t.tx) * lanes / GN_THREADS);
+    if (u > score * 1.001) {
+      score = u;
+      best = std::move(t);
+    }
+    if (cap >= V) break;
   }
-  c.colpart = at;
-  c.total = at + (op == GN_FWD ? 0 : al256(size_t(c.col_parts) * 2 * size_t(L.dim) * 8));
-  c.total = std::max<size_t>(c.total, 256);
+  return best;
+}
+
+// Work of a call: which kernel, and the thread layout.
+GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows, int op, NormArgs* a) {
+  GnConfig c;
+  a->N = N;
+  a->B = int32_t(B);
+  a->lay = f->lay;
+  const int64_t most = max_rows > 0 ? std::min(max_rows, N) : N;
+  const int RP = gn_reg_rows(op);
+  // local: the rows of the longest segment fit the registers of one CTA, or of a cluster of up to 16
+  int shift = 0;
+  if (most > 1)
+    while ((int64_t(RP) << shift) < most && shift < 8) ++shift;
+  const TileSet* t = &f->local[shift];
+  a->cs = 1;
+  if ((int64_t(RP) << shift) >= most && t->n() > 0 && t->n() <= 64) {
+    c.local = true;
+    a->k = 1 << shift;
+    a->j = std::max(1, GN_THREADS / (t->tx << shift));
+  } else if (f->cluster_ok) {
+    t = &f->grid;
+    a->k = GN_THREADS / t->tx;
+    a->j = 1;
+    while (a->cs < 16 && int64_t(RP) * a->k * a->cs < most) a->cs *= 2;
+    c.local = int64_t(RP) * a->k * a->cs >= most;
+  }
+  // few CTAs: divide the rows further, so that more SMs load them
+  if (c.local && a->j == 1 && f->cluster_ok && most > 2 * a->k) {
+    const TileSet* n = &f->grid;
+    while (a->cs < 8 && int64_t(n->n()) * B * a->cs * 2 <= 2 * sm_count() &&
+           most > int64_t(GN_THREADS / n->tx) * a->cs * 2) {
+      t = n;
+      a->k = GN_THREADS / n->tx;
+      a->cs *= 2;
+    }
+  }
+  if (!c.local) {
+    t = &f->grid;
+    a->cs = 1;
+    a->k = GN_THREADS / t->tx;
+    a->j = 1;
+  }
+  c.one_row = c.local && most <= 1;
+  std::copy(t->first.begin(), t->first.end(), a->tile);
+  a->n_tiles = t->n();
+  a->tx = t->tx;
+  a->wide = t->cut;
+  a->lanes = 1;
+  while (a->lanes < a->k * std::min(f->wide, t->tx) && a->lanes < 32) a->lanes *= 2;
   return c;
 }
 
-// Gradients of the weights and biases: column sums of all CTAs, joined in order, then added over the
-// components of a channel.  blockIdx.y: 0 weights, 1 biases.
-constexpr int CS_COLS = 1024;
-__host__ __device__ int cs_channels(int d) { return CS_COLS / d < 32 ? CS_COLS / d : 32; }
-
-template <typename T>
-__global__ void __launch_bounds__(256) gn_colsum_kernel(const double* colpart, int64_t parts, T* gw, T* gb,
-                                                        const __grid_constant__ RowLayout L) {
-  __shared__ double acc[8][33];
-  __shared__ double cols[CS_COLS];
-  int bi = 0, at = int(blockIdx.x);
-  while (true) {
-    const int n = (L.blk[bi].mul + cs_channels(L.blk[bi].d) - 1) / cs_channels(L.blk[bi].d);
-    if (at < n) break;
-    at -= n;
-    ++bi;
-  }
-  const RowBlock& b = L.blk[bi];
-  const bool bias = blockIdx.y == 1;
-  if (bias ? (gb == nullptr || b.bias0 < 0) : gw == nullptr) return;
-  const int u0 = at * cs_channels(b.d), nu = min(cs_channels(b.d), b.mul - u0), ncol = nu * b.d;
-  const int tx = int(threadIdx.x) % 32, ty = int(threadIdx.x) / 32;
-  for (int c0 = 0; c0 < ncol; c0 += 32) {
-    double s = 0.0;
-    if (c0 + tx < ncol) {
-      const double* p = colpart + (bias ? L.dim : 0) + b.col0 + u0 * b.d + c0 + tx;
-      for (int64_t i = ty; i < parts; i += 8) s += p[i * 2 * L.dim];
-    }
-    acc[ty][tx] = s;
-    __syncthreads();
-    if (ty == 0 && c0 + tx < ncol) {
-#pragma unroll
-      for (int i = 1; i < 8; ++i) s += acc[i][tx];
-      cols[c0 + tx] = s;
-    }
-    __syncthreads();
-  }
-  if (int(threadIdx.x) < nu) {
-    double s = 0.0;
-    for (int m = 0; m < b.d; ++m) s += cols[int(threadIdx.x) * b.d + m];
-    if (bias) gb[b.bias0 + u0 + threadIdx.x] = T(s);
-    else gw[b.chan0 + u0 + threadIdx.x] = T(s);
-  }
+e3_status check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 15u))
+    return fail(E3_ERR_INVALID_ARG, "workspace is NULL or not 16-byte aligned");
+  if (bytes < need) return fail(E3_ERR_SHAPE, "workspace of %zu bytes, %zu needed", bytes, need);
+  return E3_OK;
 }
 
-void launch_colsum(const e3_features* f, const GnConfig& c, const double* colpart, void* gw, void* gb, cudaStream_t s) {
-  const RowLayout& L = f->lay;
-  int n = 0;
-  for (int b = 0; b < L.n_blocks; ++b) n += (L.blk[b].mul + cs_channels(L.blk[b].d) - 1) / cs_channels(L.blk[b].d);
-  if (L.n_scalars == 0) gb = nullptr;
-  if (gw == nullptr && gb == nullptr) return;
-  const dim3 grid{unsigned(n), gb ? 2u : 1u};
-  if (f->dtype == E3_F64)
-    gn_colsum_kernel<double><<<grid, 256, 0, s>>>(colpart, c.col_parts, static_cast<double*>(gw),
-                                                  static_cast<double*>(gb), L);
-  else
-    gn_colsum_kernel<float><<<grid, 256, 0, s>>>(colpart, c.col_parts, static_cast<float*>(gw),
-                                                 static_cast<float*>(gb), L);
+size_t workspace_bytes_of(const GnConfig& c, NormArgs a, e3_dtype dtype, int op) {
+  const int64_t ctas = int64_t(GN_MAX_RESIDENT) * sm_count();
+  if (c.local) return std::max<size_t>(256, gn_local_layout(&a, op, std::max<int64_t>(1, ctas / a.n_tiles)));
+  return gn_grid_layout(&a, op, dtype == E3_F64 ? 8 : 4, ctas);
 }
 
 e3_status check_sizes(const e3_features* f, int64_t N, int64_t B, bool one_ok) {
@@ -180,22 +148,12 @@ e3_status begin(const e3_features* f, int64_t N, int64_t B, const int32_t* row_p
   if (reinterpret_cast<uintptr_t>(row_ptr) & 3u) return fail(E3_ERR_INVALID_ARG, "row_ptr is not 4-byte aligned");
   if ((st = drop_args(drop, N, &a->drop, drop_on)) != E3_OK) return st;
   *c = configure(f, N, B, max_rows, op, a);
-  if (N > 0) {
-    if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 15u))
-      return fail(E3_ERR_INVALID_ARG, "workspace is NULL or not 16-byte aligned");
-    if (ws_bytes < c->total)
-      return fail(E3_ERR_SHAPE, "workspace of %zu bytes, %zu needed", ws_bytes, c->total);
-  }
+  c->ws_bytes = ws_bytes;
+  if (N > 0 && (st = check_workspace(ws, ws_bytes, workspace_bytes_of(*c, *a, f->dtype, op))) != E3_OK) return st;
   if ((st = ensure_device_tables()) != E3_OK) return st;
   if ((st = device_status_ptr(&a->status)) != E3_OK) return st;
-  a->N = N;
-  a->B = int32_t(B);
   a->row_ptr = row_ptr;
   a->act = act;
-  a->lay = f->lay;
-  char* base = static_cast<char*>(ws);
-  a->part = reinterpret_cast<double*>(base + c->part);
-  a->coef = reinterpret_cast<double*>(base + c->coef);
   return E3_OK;
 }
 
@@ -208,6 +166,51 @@ e3_status zero_params(const e3_features* f, void* gw, void* gb, cudaStream_t s) 
 }
 
 }  // namespace
+
+void make_tiles(e3_features* f) {
+  const RowLayout& L = f->lay;
+  // 16-byte vectors need every group to be a whole number of them (then every block, and the row, is)
+  f->vec = f->dtype == E3_F64 ? 2 : 4;
+  for (int b = 0; b < L.n_blocks; ++b)
+    if (L.blk[b].group_cols % f->vec != 0) f->vec = 1;
+  for (int b = 0; b < L.n_blocks; ++b) f->wide = std::max(f->wide, L.blk[b].group_cols / f->vec);
+  for (int i = 0; i < 9; ++i)
+    if ((f->wide << i) <= GN_THREADS)
+      f->local[i] = best_tiles(L, f->vec, f->wide, GN_THREADS >> i, 1 << i);
+  // narrow tiles leave each CTA more rows, so that fewer partial sums are joined; 128 bytes at least
+  const int lo = std::min(GN_THREADS, std::max(f->wide, 8));
+  f->grid = best_tiles(L, f->vec, lo, std::max(lo, 32), 0);
+  if (f->grid.n() <= 0) f->grid = cut_tiles(L, f->vec, GN_THREADS);
+  // clusters: few tiles, none with more groups than a CTA's table of its cluster's sums holds
+  f->cluster_ok = f->grid.n() <= 64 && !f->grid.cut;
+  for (int i = 0; i < f->grid.n(); ++i)
+    if (group_of(L, f->grid.first[i + 1] * f->vec - 1) - group_of(L, f->grid.first[i] * f->vec) >= 32) f->cluster_ok = false;
+}
+
+// Bytes of one slab's inputs that are expected to stay in L2 until the second pass.
+constexpr int64_t GN_SLAB_BYTES = int64_t(32) << 20, GN_ONE_SLAB_BYTES = int64_t(64) << 20;
+
+size_t gn_grid_layout(NormArgs* a, int op, int elem, int64_t ctas) {
+  const int64_t bytes = a->N * a->lay.dim * elem * (op + 1);
+  const int64_t slabs = bytes <= GN_ONE_SLAB_BYTES ? 1 : (bytes + GN_SLAB_BYTES - 1) / GN_SLAB_BYTES;
+  a->cx = int32_t(std::max<int64_t>(1, std::min<int64_t>((a->n_tiles + slabs - 1) / slabs, ctas)));
+  const int64_t most = std::max<int64_t>(1, ctas / a->cx);
+  a->rows_cta = std::max<int64_t>((a->N + most - 1) / most, 2 * a->k);
+  a->chunks = int32_t(std::max<int64_t>(1, (a->N + a->rows_cta - 1) / a->rows_cta));
+  const size_t G = size_t(a->lay.n_groups());
+  const size_t slots = a->wide ? size_t(most) + size_t(a->B) : 2 * size_t(most);
+  const size_t coef = al256(slots * (G + size_t(a->n_tiles)) * gn_sums(op) * 8);
+  const size_t col = coef + (op == GN_FWD ? 0 : al256(size_t(a->B) * G * gn_coefs(op) * 8));
+  a->part = nullptr;
+  a->coef = reinterpret_cast<void*>(coef);   // offsets; the launcher adds the base
+  a->colpart = reinterpret_cast<double*>(col);
+  return std::max<size_t>(256, col + (op == GN_FWD ? 0 : al256(size_t(most) * 2 * size_t(a->lay.dim) * 8)));
+}
+
+size_t gn_local_layout(NormArgs* a, int op, int64_t parts) {
+  return op == GN_FWD ? 0 : al256(size_t(parts) * 2 * size_t(a->lay.dim) * 8);
+}
+
 }  // namespace e3b
 
 using namespace e3b;
@@ -221,7 +224,8 @@ extern "C" e3_status e3_group_norm_workspace_size(const e3_features* f, int64_t 
   *bytes = 0;
   for (int op = GN_FWD; op <= GN_DBL; ++op) {
     NormArgs a{};
-    *bytes = std::max(*bytes, configure(f, N, B, max_rows, op, &a).total);
+    const GnConfig c = configure(f, N, B, max_rows, op, &a);
+    *bytes = std::max(*bytes, workspace_bytes_of(c, a, f->dtype, op));
   }
   return E3_OK;
 }
@@ -249,7 +253,7 @@ extern "C" e3_status e3_group_norm_forward(const e3_features* f, int64_t N, int6
   a.o0 = y;
   a.stats = stats;
   a.eps = eps;
-  return gn_launch_fwd(a, c, f->dtype == E3_F64, on, static_cast<cudaStream_t>(stream));
+  return gn_launch_fwd(a, c, f->dtype == E3_F64, f->vec, on, workspace, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" e3_status e3_group_norm_backward(const e3_features* f, int64_t N, int64_t B, const int32_t* row_ptr,
@@ -277,13 +281,10 @@ extern "C" e3_status e3_group_norm_backward(const e3_features* f, int64_t N, int
   a.b = bias;
   a.o0 = grad_x;
   a.stats = const_cast<double*>(stats);
-  if (grad_weight || grad_bias) a.colpart = reinterpret_cast<double*>(static_cast<char*>(workspace) + c.colpart);
-  if (grad_x == nullptr && a.colpart == nullptr) return E3_OK;
-  if ((st = gn_launch_bwd(a, c, f->dtype == E3_F64, on, s)) != E3_OK) return st;
-  launch_colsum(f, c, a.colpart, grad_weight, grad_bias, s);
-  const cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess) return fail(E3_ERR_CUDA, "group norm backward launch failed: %s", cudaGetErrorString(err));
-  return E3_OK;
+  a.gw = grad_weight;
+  a.gb = f->lay.n_scalars > 0 ? grad_bias : nullptr;
+  if (a.o0 == nullptr && a.gw == nullptr && a.gb == nullptr) return E3_OK;
+  return gn_launch_bwd(a, c, f->dtype == E3_F64, f->vec, on, workspace, s);
 }
 
 extern "C" e3_status e3_group_norm_double_backward(const e3_features* f, int64_t N, int64_t B, const int32_t* row_ptr,
@@ -317,12 +318,8 @@ extern "C" e3_status e3_group_norm_double_backward(const e3_features* f, int64_t
   a.o0 = d_x;
   a.o1 = d_grad_y;
   a.stats = const_cast<double*>(stats);
-  if (d_weight || d_bias) a.colpart = reinterpret_cast<double*>(static_cast<char*>(workspace) + c.colpart);
-  if (d_x == nullptr && d_grad_y == nullptr && a.colpart == nullptr) return E3_OK;
-  if ((st = gn_launch_dbl(a, c, f->dtype == E3_F64, on, s)) != E3_OK) return st;
-  launch_colsum(f, c, a.colpart, d_weight, d_bias, s);
-  const cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess)
-    return fail(E3_ERR_CUDA, "group norm double backward launch failed: %s", cudaGetErrorString(err));
-  return E3_OK;
+  a.gw = d_weight;
+  a.gb = f->lay.n_scalars > 0 ? d_bias : nullptr;
+  if (a.o0 == nullptr && a.o1 == nullptr && a.gw == nullptr && a.gb == nullptr) return E3_OK;
+  return gn_launch_dbl(a, c, f->dtype == E3_F64, f->vec, on, workspace, s);
 }

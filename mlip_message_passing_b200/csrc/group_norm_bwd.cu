@@ -1,7 +1,7 @@
 #include "group_norm_launch.h"
 
 namespace e3b {
-e3_status gn_launch_bwd(const NormArgs& a, const GnConfig& c, bool f64, bool drop, cudaStream_t s) {
-  return gn_launch<GN_BWD>(a, c, f64, drop, s);
+e3_status gn_launch_bwd(NormArgs& a, const GnConfig& c, bool f64, int vec, bool drop, void* ws, cudaStream_t s) {
+  return gn_launch<GN_BWD>(a, c, f64, vec, drop, ws, s);
 }
 }  // namespace e3b

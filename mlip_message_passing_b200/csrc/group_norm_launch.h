@@ -1,51 +1,152 @@
-// Launch configuration of the group norm and its per-form launchers (one translation unit each).
+// Launchers of the group norm, one translation unit per form.
 #pragma once
+
+#include <atomic>
 
 #include "group_norm.cuh"
 
 namespace e3b {
 
+static_assert(sizeof(NormArgs) <= 4096, "kernel arguments");
+
 struct GnConfig {
   bool local = false;
-  int vec = 1;
-  int64_t col_parts = 0;  // slots of colpart
-  dim3 grid;              // local kernel, or both passes of split
-  // workspace layout (bytes)
-  size_t part = 0, coef = 0, colpart = 0, total = 0;
+  bool one_row = false;   // local: no segment has more than one row
+  int64_t max_ctas = 0;   // local: CTAs along the segments that have work
+  size_t ws_bytes = 0;
 };
-// rows of a segment that a thread of the local kernel keeps in registers
+// rows that a thread of the local kernel keeps in registers; segments that share them when every
+// segment is one row
 __host__ __device__ constexpr int gn_reg_rows(int op) { return op == GN_DBL ? 4 : 8; }
+__host__ __device__ constexpr int gn_reg_segments(int op) { return op == GN_FWD ? 8 : op == GN_BWD ? 4 : 2; }
 
-e3_status gn_launch_fwd(const NormArgs& a, const GnConfig& c, bool f64, bool drop, cudaStream_t s);
-e3_status gn_launch_bwd(const NormArgs& a, const GnConfig& c, bool f64, bool drop, cudaStream_t s);
-e3_status gn_launch_dbl(const NormArgs& a, const GnConfig& c, bool f64, bool drop, cudaStream_t s);
+// Chunks and workspace of the grid kernel on `ctas` resident CTAs; returns the bytes needed.
+size_t gn_grid_layout(NormArgs* a, int op, int elem, int64_t ctas);
+size_t gn_local_layout(NormArgs* a, int op, int64_t parts);
+// Most CTAs that any kernel here keeps resident on an SM (sizes workspaces).
+constexpr int GN_MAX_RESIDENT = 8;
+
+e3_status gn_launch_fwd(NormArgs& a, const GnConfig& c, bool f64, int vec, bool drop, void* ws, cudaStream_t s);
+e3_status gn_launch_bwd(NormArgs& a, const GnConfig& c, bool f64, int vec, bool drop, void* ws, cudaStream_t s);
+e3_status gn_launch_dbl(NormArgs& a, const GnConfig& c, bool f64, int vec, bool drop, void* ws, cudaStream_t s);
+
+// CTAs of `kernel` that are resident together on the current device (found once per device).
+template <typename K>
+int gn_resident(K kernel, size_t smem, std::atomic<int>* cache, bool cluster) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  int n = dev < 64 ? cache[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    int per = 0;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+      return 0;
+    if (cluster && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, GN_THREADS, smem) != cudaSuccess) return 0;
+    n = std::min(per, GN_MAX_RESIDENT) * sm_count();
+    if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+template <typename K>
+e3_status gn_start(K kernel, const NormArgs& a, dim3 grid, size_t smem, bool meet, int cluster, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(GN_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (meet) {
+    attr[n].id = cudaLaunchAttributeCooperative;
+    attr[n++].val.cooperative = 1;
+  }
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = unsigned(cluster);
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a);
+  if (err != cudaSuccess) return fail(E3_ERR_CUDA, "group norm launch failed: %s", cudaGetErrorString(err));
+  return E3_OK;
+}
+
+template <typename T, int VEC, int OP, bool DROP, int R, int M, bool CL>
+e3_status gn_run_local(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s) {
+  static std::atomic<int> cache[64];
+  constexpr size_t smem = GnLocal<T, VEC, OP, R, M, CL>::smem;
+  auto kernel = gn_local_kernel<T, VEC, OP, DROP, R, M, CL>;
+  const int q = gn_resident(kernel, smem, cache, CL);
+  int64_t room = q / a.n_tiles / a.cs;  // clusters along the segments that are resident together
+  if (CL) {
+    static std::atomic<int> clusters[64][5];
+    int dev = 0, size = 0;
+    cudaGetDevice(&dev);
+    while ((1 << size) < a.cs) ++size;
+    int n = dev < 64 ? clusters[dev][size].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(unsigned(a.cs));
+      cfg.blockDim = dim3(GN_THREADS);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = unsigned(a.cs);
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      if (q == 0 || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+      if (dev < 64) clusters[dev][size].store(n, std::memory_order_relaxed);
+    }
+    room = std::min<int64_t>(room, n / a.n_tiles);
+    if (OP == GN_FWD && n > 0) room = std::max<int64_t>(room, 1);  // nothing here waits for other clusters
+  }
+  if (room < 1) return fail(E3_ERR_CUDA, "group norm: no room for the kernel on this device");
+  const int64_t batch = int64_t(a.j) * M;
+  const int64_t parts = std::min<int64_t>((a.B + batch - 1) / batch, room) * a.cs;
+  if (gn_local_layout(&a, OP, parts) > c.ws_bytes) return fail(E3_ERR_SHAPE, "group norm: workspace too small");
+  const bool columns = OP != GN_FWD && (a.gw != nullptr || a.gb != nullptr);
+  a.colpart = columns ? static_cast<double*>(ws) : nullptr;
+  return gn_start(kernel, a, dim3(unsigned(parts), unsigned(a.n_tiles)), smem, columns, a.cs, s);
+}
 
 template <typename T, int VEC, int OP, bool DROP>
-void gn_run(const NormArgs& a, const GnConfig& c, cudaStream_t s) {
+e3_status gn_run(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s) {
   if (c.local) {
-    gn_local_kernel<T, VEC, OP, DROP, gn_reg_rows(OP)><<<c.grid, GN_THREADS, 0, s>>>(a);
-    return;
+    if (c.one_row) return gn_run_local<T, VEC, OP, DROP, 1, gn_reg_segments(OP), false>(a, c, ws, s);
+    if (a.cs > 1) return gn_run_local<T, VEC, OP, DROP, gn_reg_rows(OP), 1, true>(a, c, ws, s);
+    return gn_run_local<T, VEC, OP, DROP, gn_reg_rows(OP), 1, false>(a, c, ws, s);
   }
-  gn_partial_kernel<T, VEC, OP, DROP><<<c.grid, GN_THREADS, 0, s>>>(a);
-  const int64_t warps = int64_t(a.B) * a.lay.n_groups();
-  gn_final_kernel<OP, VEC><<<unsigned((warps * 32 + GN_THREADS - 1) / GN_THREADS), GN_THREADS, 0, s>>>(a);
-  if (OP != GN_BWD || a.o0 != nullptr) gn_apply_kernel<T, VEC, OP, DROP><<<c.grid, GN_THREADS, 0, s>>>(a);
+  static std::atomic<int> cache[64];
+  constexpr size_t smem = GnGrid<T, VEC, OP>::smem;
+  auto kernel = gn_grid_kernel<T, VEC, OP, DROP>;
+  const int q = gn_resident(kernel, smem, cache, false);
+  if (q == 0) return fail(E3_ERR_CUDA, "group norm: no room for the kernel on this device");
+  if (gn_grid_layout(&a, OP, int(sizeof(T)), q) > c.ws_bytes)
+    return fail(E3_ERR_SHAPE, "group norm: workspace too small");
+  char* base = static_cast<char*>(ws);
+  a.part = base;
+  a.coef = base + reinterpret_cast<size_t>(a.coef);
+  const bool columns = OP != GN_FWD && (a.gw != nullptr || a.gb != nullptr);
+  a.colpart = columns ? reinterpret_cast<double*>(base + reinterpret_cast<size_t>(a.colpart)) : nullptr;
+  return gn_start(kernel, a, dim3(unsigned(a.chunks) * unsigned(a.cx)), smem, true, 1, s);
 }
 
 template <int OP>
-e3_status gn_launch(const NormArgs& a, const GnConfig& c, bool f64, bool drop, cudaStream_t s) {
-#define GN_CASE(T, V) (drop ? gn_run<T, V, OP, true>(a, c, s) : gn_run<T, V, OP, false>(a, c, s))
+e3_status gn_launch(NormArgs& a, const GnConfig& c, bool f64, int vec, bool drop, void* ws, cudaStream_t s) {
+#define GN_CASE(T, V) return drop ? gn_run<T, V, OP, true>(a, c, ws, s) : gn_run<T, V, OP, false>(a, c, ws, s)
   if (f64) {
-    if (c.vec == 2) GN_CASE(double, 2);
-    else GN_CASE(double, 1);
-  } else {
-    if (c.vec == 4) GN_CASE(float, 4);
-    else GN_CASE(float, 1);
+    if (vec == 2) GN_CASE(double, 2);
+    GN_CASE(double, 1);
   }
+  if (vec == 4) GN_CASE(float, 4);
+  GN_CASE(float, 1);
 #undef GN_CASE
-  const cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess) return fail(E3_ERR_CUDA, "group norm launch failed: %s", cudaGetErrorString(err));
-  return E3_OK;
 }
 
 }  // namespace e3b

@@ -24,22 +24,24 @@ __device__ __forceinline__ void store_row(T* p, const RowVec<T, VEC>& v) {
   *reinterpret_cast<RowVec<T, VEC>*>(p) = v;
 }
 
+__host__ __device__ __forceinline__ uint32_t fast_div(uint32_t x, uint32_t recip) {
+#ifdef __CUDA_ARCH__
+  return recip ? __umulhi(x, recip) : x;
+#else
+  return recip ? uint32_t((uint64_t(x) * recip) >> 32) : x;
+#endif
+}
+
 // Block of a column.
-__device__ __forceinline__ int block_of(const RowLayout& L, int col) {
+__host__ __device__ __forceinline__ int block_of(const RowLayout& L, int col) {
   int b = 0;
   while (b + 1 < L.n_blocks && col >= L.blk[b + 1].col0) ++b;
   return b;
 }
 // Group index (over all blocks) of a column.
 __host__ __device__ __forceinline__ int group_of(const RowLayout& L, int col) {
-  int b = 0;
-  while (b + 1 < L.n_blocks && col >= L.blk[b + 1].col0) ++b;
-  return b * L.groups + (col - L.blk[b].col0) / L.blk[b].group_cols;
-}
-// First column of a group.
-__host__ __device__ __forceinline__ int group_col(const RowLayout& L, int g) {
-  const RowBlock& b = L.blk[g / L.groups];
-  return b.col0 + (g % L.groups) * b.group_cols;
+  const int b = block_of(L, col);
+  return b * L.groups + int(fast_div(uint32_t(col - L.blk[b].col0), L.blk[b].div_group));
 }
 
 // Philox4x32-10 (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3"): ten rounds of two
@@ -66,12 +68,12 @@ struct DropCol {
 
   __device__ __forceinline__ void init(const RowLayout& L, const DropArgs& a, int col) {
     const int b = block_of(L, col);
-    const int o = col - L.blk[b].col0, d = L.blk[b].d;
+    const uint32_t o = uint32_t(col - L.blk[b].col0);
     block = uint32_t(b);
-    quad = uint32_t(o / d) >> 2;
+    quad = fast_div(o, L.blk[b].div_d) >> 2;
     sel = 0;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) sel |= (uint32_t((o + i) / d) & 3u) << (2 * i);
+    for (int i = 0; i < VEC; ++i) sel |= (fast_div(o + i, L.blk[b].div_d) & 3u) << (2 * i);
     k0 = a.k0;
     k1 = a.k1;
     offset = a.offset;

@@ -698,8 +698,8 @@ class Features:
 class Segments:
     """Rows of a batch cut into structures: segment s holds rows row_ptr[s] .. row_ptr[s+1] - 1 of
     ``n_rows``; rows from row_ptr[-1] on are padding.  ``row_ptr``: int32 CUDA tensor [B + 1] starting
-    at 0.  ``max_rows``: an upper bound on a segment's rows if the host knows one (it selects the
-    kernels; results do not depend on it)."""
+    at 0.  ``max_rows``: an upper bound on a segment's rows if the host knows one: it selects the
+    kernels (a bound that does not hold is reported by ``device_status``)."""
 
     def __init__(self, row_ptr, n_rows, max_rows=None):
         if not isinstance(row_ptr, torch.Tensor) or row_ptr.dim() != 1 or row_ptr.shape[0] < 2:

@@ -112,12 +112,26 @@ def test_norm_long_segments(e3b, irreps, groups, counts, pad, dtype):
 @pytest.mark.parametrize("irreps,groups", [LAYOUTS[0], LAYOUTS[3]])
 @pytest.mark.parametrize("counts,pad,hint", [
     ([5, 0, 1, 17, 2, 9, 0, 60], 3, 0),    # no hint: the kernels for long segments on short ones
-    ([150, 0, 301, 40], 5, 1),             # a hint that is far too small is still only a hint
+    ([150, 0, 301, 40], 5, 400),           # a bound that is not tight
+    ([70, 0, 3, 64], 5, 2000),             # nor this one: clusters with idle CTAs
     ([1] * 200, 0, "max"),                 # every row by itself
     ([0, 0, 0], 4, "max"),                 # nothing but padding
 ])
 def test_norm_hints_and_rows(e3b, irreps, groups, counts, pad, hint):
     _check_all(e3b, irreps, groups, counts, pad, torch.float32, "silu", 0.0, seed=21, hint=hint)
+
+
+def test_norm_bound_that_is_too_small_is_reported(e3b):
+    """Rows of a segment beyond what the bound selected are skipped and the status word says so."""
+    f = e3b.Features("8x0e+8x1o", groups=2)
+    x = torch.randn(500, 32, device=DEV)
+    seg = e3b.Segments.from_counts([200, 300])
+    for bound in (1, 2, 7):
+        seg.max_rows = bound
+        e3b.group_norm_forward(f, x, segments=seg)
+        with pytest.raises(e3b.E3Error) as err:
+            e3b.device_status()
+        assert err.value.status == e3b.E3_ERR_INDEX
 
 
 def test_norm_wide_groups(e3b):
