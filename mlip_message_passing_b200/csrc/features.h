@@ -51,11 +51,10 @@ void make_tiles(e3_features* f);
 // f is not NULL and its device is current.
 e3_status check_features_device(const e3_features* f);
 
-// A cut of a row's vector columns into tiles of at most tx: whole groups, or parts of one group that is
-// wider than a block of threads (`cut`).
+// A cut of a row's vector columns into tiles of at most tx.
 struct TileSet {
-  int tx = 0;
-  bool cut = false;
+  int tx = 0, groups = 0;      // widest tile, most groups of a tile
+  bool cut = false;            // some group lies in several tiles
   std::vector<int32_t> first;  // first vector column of each tile, then the end
   int n() const { return int(first.size()) - 1; }
 };
@@ -69,5 +68,6 @@ struct e3_features {
   int vec = 1;                   // group norm: columns of a vector
   bool cluster_ok = false;       // group norm: the tiles for long segments suit clusters
   int wide = 0;                  // widest group in vectors
-  e3b::TileSet local[9], grid;   // tiles for 2^i row lanes of a segment; for long segments
+  // tiles for 2^i row lanes of a segment, for segments of one row, for clusters, for long segments
+  e3b::TileSet local[9], rows, narrow, grid;
 };

@@ -8,44 +8,66 @@ namespace {
 
 size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 
-// Cut the row into tiles of at most `cap` vectors: groups in order, as many as fit; a group wider than
-// cap is cut at whole channels (a channel is d columns; a vector holds parts of whole quads).
+void count_groups(const RowLayout& L, int vec, TileSet* t) {
+  for (int i = 0; i + 1 < int(t->first.size()); ++i) {
+    const int a = t->first[i] * vec, b = t->first[i + 1] * vec - 1;
+    t->tx = std::max(t->tx, t->first[i + 1] - t->first[i]);
+    t->groups = std::max(t->groups, group_of(L, b) - group_of(L, a) + 1);
+    if (i > 0 && group_of(L, a - 1) == group_of(L, a)) t->cut = true;
+  }
+}
+
+// Tiles of whole groups, as many as fit `cap` vectors (cap >= the widest group).
 TileSet cut_tiles(const RowLayout& L, int vec, int cap) {
   TileSet t;
   t.first.push_back(0);
   int at = 0;
   for (int b = 0; b < L.n_blocks; ++b) {
-    const int w = L.blk[b].group_cols / vec, d = L.blk[b].d;
+    const int w = L.blk[b].group_cols / vec;
     for (int g = 0; g < L.groups; ++g) {
       if (at + w - t.first.back() > cap && at > t.first.back()) t.first.push_back(at);
-      if (w > cap) {
-        const int step = std::max(1, cap / d) * d;
-        for (int o = step; o < w; o += step) t.first.push_back(at + o);
-        t.cut = true;
-        at += w;
-        t.first.push_back(at);
-      } else {
-        at += w;
-      }
+      at += w;
     }
   }
-  if (t.first.back() != at) t.first.push_back(at);
-  for (int i = 0; i + 1 < int(t.first.size()); ++i) t.tx = std::max(t.tx, t.first[i + 1] - t.first[i]);
+  t.first.push_back(at);
+  count_groups(L, vec, &t);
   return t;
 }
 
-// The cut between `lo` and `hi` that leaves the fewest of a block's threads idle (the narrowest of equals).
-TileSet best_tiles(const RowLayout& L, int vec, int lo, int hi, int k) {
+// Equal tiles wherever they end: the widest of those that leave the fewest of a block's threads idle.
+TileSet equal_tiles(const RowLayout& L, int vec) {
+  const int V = L.dim / vec;
+  int best = 0;
+  double score = 0.0;
+  for (int n = (V + GN_THREADS - 1) / GN_THREADS; n <= std::min(V, 256); ++n) {
+    const int tx = (V + n - 1) / n, lanes = GN_THREADS / tx;
+    const double u = double(V) / (double((V + tx - 1) / tx) * tx) * (double(tx) * lanes / GN_THREADS);
+    if (u > score * 1.03) {
+      score = u;
+      best = tx;
+    }
+    if (tx <= 32) break;
+  }
+  TileSet t;
+  for (int v = 0; v < V; v += best) t.first.push_back(v);
+  t.first.push_back(V);
+  count_groups(L, vec, &t);
+  return t;
+}
+
+// The cut between `lo` and `hi` that leaves the fewest of a block's threads idle; of cuts within 3% of it the
+// widest, whose rows are the longest runs of memory.
+TileSet best_tiles(const RowLayout& L, int vec, int lo, int hi, int k, int threads) {
   TileSet best;
   double score = -1.0;
   const int V = L.dim / vec;
   for (int cap = lo; cap <= hi; ++cap) {
     TileSet t = cut_tiles(L, vec, cap);
     if (t.n() > GN_MAXTILE) continue;
-    const int lanes = k > 0 ? k * std::max(1, GN_THREADS / (t.tx * k)) : GN_THREADS / t.tx;
-    const double u = double(V) / (double(t.n()) * t.tx) * (double(t.tx) * lanes / GN_THREADS);
-    if (u > score * 1.001) {
-      score = u;
+    const int lanes = k > 0 ? k * std::max(1, threads / (t.tx * k)) : threads / t.tx;
+    const double u = double(V) / (double(t.n()) * t.tx) * (double(t.tx) * lanes / threads);
+    if (u >= score * 0.97) {
+      score = std::max(score, u);
       best = std::move(t);
     }
     if (cap >= V) break;
@@ -61,31 +83,39 @@ GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows,
   a->lay = f->lay;
   const int64_t most = max_rows > 0 ? std::min(max_rows, N) : N;
   const int RP = gn_reg_rows(op);
-  // local: the rows of the longest segment fit the registers of one CTA, or of a cluster of up to 16
+  // local: the rows of the longest segment fit one CTA, or a cluster of up to 16
   int shift = 0;
-  if (most > 1)
-    while ((int64_t(RP) << shift) < most && shift < 8) ++shift;
+  while ((int64_t(RP) << shift) < most && shift < 8) ++shift;
   const TileSet* t = &f->local[shift];
+  int threads = GN_THREADS;
   a->cs = 1;
-  if ((int64_t(RP) << shift) >= most && t->n() > 0 && t->n() <= 64) {
+  if (most <= 1 && f->rows.n() > 0 && f->rows.n() <= 64) {
+    c.local = c.one_row = true;
+    t = &f->rows;
+    threads = GN_ROW_THREADS;
+    a->k = 1;
+    a->j = threads / t->tx;
+  } else if ((int64_t(RP) << shift) >= most && t->n() > 0 && t->n() <= 64) {
     c.local = true;
     a->k = 1 << shift;
     a->j = std::max(1, GN_THREADS / (t->tx << shift));
-  } else if (f->cluster_ok) {
-    t = &f->grid;
-    a->k = GN_THREADS / t->tx;
-    a->j = 1;
-    while (a->cs < 16 && int64_t(RP) * a->k * a->cs < most) a->cs *= 2;
-    c.local = int64_t(RP) * a->k * a->cs >= most;
   }
-  // few CTAs: divide the rows further, so that more SMs load them
-  if (c.local && a->j == 1 && f->cluster_ok && most > 2 * a->k) {
-    const TileSet* n = &f->grid;
-    while (a->cs < 8 && int64_t(n->n()) * B * a->cs * 2 <= 2 * sm_count() &&
-           most > int64_t(GN_THREADS / n->tx) * a->cs * 2) {
+  // clusters: when one CTA is too small, or when there are so few CTAs that dividing the rows further lets
+  // more SMs load them
+  if (f->cluster_ok && !c.one_row) {
+    const TileSet* n = &f->narrow;
+    const int k = GN_THREADS / n->tx;
+    int cs = 1;
+    while (cs < 16 && int64_t(RP) * k * cs < most) cs *= 2;
+    // the backwards' clusters meet for the parameters' gradients: one per tile has to be resident
+    const bool fits = int64_t(RP) * k * cs >= most && (op == GN_FWD || n->n() * cs <= 128);
+    if (fits && (!c.local || (a->j == 1 && int64_t(t->n()) * B < sm_count()))) {
+      while (cs < 8 && int64_t(n->n()) * B * cs * 2 <= (op == GN_FWD ? 2 * sm_count() : 128) && most > 2 * k * cs) cs *= 2;
+      c.local = true;
       t = n;
-      a->k = GN_THREADS / n->tx;
-      a->cs *= 2;
+      a->k = k;
+      a->j = 1;
+      a->cs = cs;
     }
   }
   if (!c.local) {
@@ -94,11 +124,11 @@ GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows,
     a->k = GN_THREADS / t->tx;
     a->j = 1;
   }
-  c.one_row = c.local && most <= 1;
   std::copy(t->first.begin(), t->first.end(), a->tile);
   a->n_tiles = t->n();
   a->tx = t->tx;
   a->wide = t->cut;
+  a->tile_groups = t->groups;
   a->lanes = 1;
   while (a->lanes < a->k * std::min(f->wide, t->tx) && a->lanes < 32) a->lanes *= 2;
   return c;
@@ -176,25 +206,18 @@ void make_tiles(e3_features* f) {
   for (int b = 0; b < L.n_blocks; ++b) f->wide = std::max(f->wide, L.blk[b].group_cols / f->vec);
   for (int i = 0; i < 9; ++i)
     if ((f->wide << i) <= GN_THREADS)
-      f->local[i] = best_tiles(L, f->vec, f->wide, GN_THREADS >> i, 1 << i);
-  // narrow tiles leave each CTA more rows, so that fewer partial sums are joined; 128 bytes at least
-  const int lo = std::min(GN_THREADS, std::max(f->wide, 8));
-  f->grid = best_tiles(L, f->vec, lo, std::max(lo, 32), 0);
-  if (f->grid.n() <= 0) f->grid = cut_tiles(L, f->vec, GN_THREADS);
+      f->local[i] = best_tiles(L, f->vec, f->wide, GN_THREADS >> i, 1 << i, GN_THREADS);
+  if (f->wide <= GN_ROW_THREADS) f->rows = best_tiles(L, f->vec, f->wide, GN_ROW_THREADS, 1, GN_ROW_THREADS);
+  f->grid = equal_tiles(L, f->vec);
+  // narrow tiles for clusters, which leave the CTAs more row lanes
+  if (f->wide <= 64) f->narrow = cut_tiles(L, f->vec, std::max(f->wide, 8));
   // clusters: few tiles, none with more groups than a CTA's table of its cluster's sums holds
-  f->cluster_ok = f->grid.n() <= 64 && !f->grid.cut;
-  for (int i = 0; i < f->grid.n(); ++i)
-    if (group_of(L, f->grid.first[i + 1] * f->vec - 1) - group_of(L, f->grid.first[i] * f->vec) >= 32) f->cluster_ok = false;
+  f->cluster_ok = f->narrow.n() > 0 && f->narrow.n() <= 64 && f->narrow.groups <= 32;
 }
 
-// Bytes of one slab's inputs that are expected to stay in L2 until the second pass.
-constexpr int64_t GN_SLAB_BYTES = int64_t(32) << 20, GN_ONE_SLAB_BYTES = int64_t(64) << 20;
-
 size_t gn_grid_layout(NormArgs* a, int op, int elem, int64_t ctas) {
-  const int64_t bytes = a->N * a->lay.dim * elem * (op + 1);
-  const int64_t slabs = bytes <= GN_ONE_SLAB_BYTES ? 1 : (bytes + GN_SLAB_BYTES - 1) / GN_SLAB_BYTES;
-  a->cx = int32_t(std::max<int64_t>(1, std::min<int64_t>((a->n_tiles + slabs - 1) / slabs, ctas)));
-  const int64_t most = std::max<int64_t>(1, ctas / a->cx);
+  (void)elem;
+  const int64_t most = std::max<int64_t>(1, ctas / a->n_tiles);
   a->rows_cta = std::max<int64_t>((a->N + most - 1) / most, 2 * a->k);
   a->chunks = int32_t(std::max<int64_t>(1, (a->N + a->rows_cta - 1) / a->rows_cta));
   const size_t G = size_t(a->lay.n_groups());

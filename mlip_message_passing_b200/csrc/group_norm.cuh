@@ -15,10 +15,9 @@
 // O(N dim), so the kernels are bound by memory, and the second pass has to find the rows on chip.
 // Two kernels, one launch each:
 //   local  a CTA, or a cluster of CTAs that divide the rows, holds whole segments x whole groups in
-//          registers between the passes (one read);
-//   grid   longer segments: a resident grid takes a slab of columns after another; in each, row chunks x
-//          column tiles publish partial sums, the grid meets, and every CTA joins the sums that it
-//          needs and reads its rows again, from L2 if the slab is small enough.
+//          shared memory between the passes (one read);
+//   grid   longer segments: the CTAs of a resident grid leave partial sums of row chunks x column
+//          tiles, meet, join them, meet, and read their rows again.
 // Sums run in the rows' type over a few rows of a thread (at most GN_FLUSH; the grid kernel goes on in
 // double from there), then over the threads, CTAs and chunks of a segment in a fixed order.  Variances are
 // sums around a thread's own mean, joined by the distances of the means, all taken from one
@@ -59,7 +58,7 @@ struct NormArgs {
   void *gw, *gb;           // gradients of weight and bias (may be NULL)
   double* stats;           // [B][groups][2]
   void* part;              // grid: partial sums, see gn_slot
-  void* coef;              // grid: [B][groups][coefs] of segments that lie inside one chunk (backwards)
+  void* coef;              // grid: [B][groups][coefs] (backwards)
   double* colpart;         // [parts][2][dim]: sums for gw, gb per column (NULL: not wanted)
   double eps;
   int32_t act;
@@ -67,7 +66,8 @@ struct NormArgs {
   int32_t tx, k, j, lanes;  // thread layout: columns, row lanes of a segment, segments, lanes of a join
   int32_t cs;               // local: CTAs of a cluster
   int32_t wide;             // grid: some group is cut into several tiles
-  int32_t n_tiles, cx;      // tiles of columns, tiles of a slab
+  int32_t n_tiles;          // tiles of columns
+  int32_t tile_groups;      // most groups that a tile holds (parts of)
   int32_t chunks;           // grid: row chunks
   int64_t rows_cta;         // grid: rows of a chunk
   DropArgs drop;
@@ -162,19 +162,62 @@ template <typename T, int VEC>
 struct GnRow {
   RowVec<T, VEC> x, g, u;
 };
-template <typename T, int VEC, int OP>
-__device__ __forceinline__ void gn_load(const NormArgs& a, int64_t at, GnRow<T, VEC>& v) {
-  v.x = load_row<T, VEC>(static_cast<const T*>(a.x) + at);
-  if (OP != GN_FWD) v.g = load_row<T, VEC>(static_cast<const T*>(a.g) + at);
-  if (OP == GN_DBL) {
-    if (a.u != nullptr) {
-      v.u = load_row<T, VEC>(static_cast<const T*>(a.u) + at);
-    } else {
+
+// Rows on their way through shared memory.  Every thread copies (cp.async) the vectors it will read
+// itself into slots of its own, so no barrier is needed, and many rows are in flight without
+// registers: slot i of a thread holds its vectors of one row, at base + i * SLOT.
+template <typename T, int VEC, int OP, int NT = GN_THREADS>
+struct GnSlots {
+  static constexpr int ARRAYS = OP + 1;
+  static constexpr int LANE = int(sizeof(T)) * VEC;        // bytes of a vector
+  static constexpr int SLOT = ARRAYS * LANE * NT;  // bytes of a slot of all threads
+  unsigned char* base;  // this thread's vector of slot 0
+  const unsigned char *x, *g, *u;
+
+  __device__ __forceinline__ void init(const NormArgs& a, unsigned char* smem) {
+    base = smem + int(threadIdx.x) * LANE;
+    x = static_cast<const unsigned char*>(a.x);
+    g = static_cast<const unsigned char*>(a.g);
+    u = static_cast<const unsigned char*>(a.u);
+  }
+  static __device__ __forceinline__ void copy(unsigned char* to, const unsigned char* from) {
+    const uint32_t d = uint32_t(__cvta_generic_to_shared(to));
+    if constexpr (LANE == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(from) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(from), "n"(LANE) : "memory");
+  }
+  // start copying the vectors at byte `at` of the rows
+  __device__ __forceinline__ void fetch(int slot, int64_t at) const {
+    unsigned char* to = base + slot * SLOT;
+    copy(to, x + at);
+    if (OP != GN_FWD) copy(to + LANE * NT, g + at);
+    if (OP == GN_DBL && u != nullptr) copy(to + 2 * LANE * NT, u + at);
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  template <int N>
+  static __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+  }
+  __device__ __forceinline__ RowVec<T, VEC> get(int slot, int array) const {
+    return load_row<T, VEC>(reinterpret_cast<const T*>(base + slot * SLOT + array * LANE * NT));
+  }
+  __device__ __forceinline__ void read(int slot, GnRow<T, VEC>& v) const {
+    v.x = get(slot, 0);
+    if (OP != GN_FWD) v.g = get(slot, 1);
+    if (OP == GN_DBL) {
+      if (u != nullptr) {
+        v.u = get(slot, 2);
+      } else {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v.u.v[i] = T(0);
+        for (int i = 0; i < VEC; ++i) v.u.v[i] = T(0);
+      }
     }
   }
-}
+  __device__ __forceinline__ void write(int slot, int array, const RowVec<T, VEC>& v) const {
+    store_row<T, VEC>(reinterpret_cast<T*>(base + slot * SLOT + array * LANE * NT), v);
+  }
+};
 
 // h, q's factor m g a''(t), m a'(t) and z of one value
 template <typename T>
@@ -279,26 +322,29 @@ struct GnAcc<T, VEC, GN_DBL, DROP> {
   }
 };
 
-// The second pass' coefficients of a (segment, group) from its joined sums S and its n values.
-// Forward: o = {mean high, mean low, r}, and (mean, r) into sg.
+__device__ __forceinline__ float gn_rsqrt(float v) {
+  const float r = rsqrtf(v);
+  return fmaf(0.5f * r, fmaf(-v * r, r, 1.f), r);  // one Newton step: the hardware's result is 2 ulp off
+}
+__device__ __forceinline__ double gn_rsqrt(double v) { return 1.0 / sqrt(v); }
+__device__ __forceinline__ float gn_recip(float v) { return __fdividef(1.f, v); }
+__device__ __forceinline__ double gn_recip(double v) { return 1.0 / v; }
+
+// The second pass' coefficients of a (segment, group) from its joined sums S and its n values.  `r` is the
+// stored one (double backward only).
 template <int OP, typename T>
-__device__ __forceinline__ void gn_finish(const T* s, T n, bool scalar, double* sg, bool keep, double eps, T* o) {
-  const T in = n > T(0) ? T(1) / n : T(0);
+__device__ __forceinline__ void gn_finish(const T* s, T n, bool scalar, T r, T eps, T* o) {
+  const T in = n > T(0) ? gn_recip(n) : T(0);
   if (OP == GN_FWD) {
-    const double mean = double(s[0]) + double(s[1]);
-    const T r = T(1) / sqrt(s[2] * in + T(eps));
-    o[0] = T(mean);
-    o[1] = T(mean - double(o[0]));
-    o[2] = r;
-    if (keep) {
-      sg[0] = mean;
-      sg[1] = double(r);
-    }
+    // pivot + (mean - pivot) as a high and a low part (their exact sum: Knuth, TAOCP 2, 4.2.2)
+    const T hi = s[0] + s[1], back = hi - s[0];
+    o[0] = hi;
+    o[1] = (s[0] - (hi - back)) + (s[1] - back);
+    o[2] = gn_rsqrt(s[2] * in + eps);
   } else if (OP == GN_BWD) {
     o[0] = scalar ? s[0] * in : T(0);
     o[1] = s[1] * in;
   } else {
-    const T r = T(sg[1]);
     const T m1 = scalar ? s[0] * in : T(0), m2 = s[1] * in, mcz = s[3] * in;
     o[0] = m1;
     o[1] = m2;
@@ -307,6 +353,12 @@ __device__ __forceinline__ void gn_finish(const T* s, T n, bool scalar, double* 
     o[4] = in * (r * (s[9] - m1 * s[6] - m2 * s[7]) + s[11] - r * m2 * s[3] - r * mcz * s[1]);
     o[5] = in * (r * (s[4] - m1 * s[2] - m2 * s[3]));
   }
+}
+// (mean, r) of the forward as the caller keeps them.
+template <typename T>
+__device__ __forceinline__ void gn_store_stats(const T* o, double* sg) {
+  sg[0] = double(o[0]) + double(o[1]);
+  sg[1] = double(o[2]);
 }
 
 // Pointwise result of one vector.  In the backward x and g hold z and c.
@@ -322,14 +374,14 @@ __device__ __forceinline__ void gn_apply(const NormArgs& a, const GnCol<T, VEC, 
       if (KIND != GN_PLAIN) t += c.b[i];
       o.v[i] = c.drop(kp, i, KIND == GN_ACT ? t * gn_sigmoid(t) : t);
     }
-    store_row<T, VEC>(static_cast<T*>(a.o0) + at, o);
+    store_row_last<T, VEC>(static_cast<T*>(a.o0) + at, o);
   } else if constexpr (OP == GN_BWD) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       const T d = v.g.v[i] - v.x.v[i] * k[1];
       o.v[i] = st.r * (KIND == GN_PLAIN ? d : d - k[0]);
     }
-    if (a.o0 != nullptr) store_row<T, VEC>(static_cast<T*>(a.o0) + at, o);
+    if (a.o0 != nullptr) store_row_last<T, VEC>(static_cast<T*>(a.o0) + at, o);
   } else {
     const uint32_t kp = c.keep(row);
     RowVec<T, VEC> dg;
@@ -346,8 +398,8 @@ __device__ __forceinline__ void gn_apply(const NormArgs& a, const GnCol<T, VEC, 
       cw[i] += q * e.z + e.h * zd;
       cb[i] += q;
     }
-    if (a.o0 != nullptr) store_row<T, VEC>(static_cast<T*>(a.o0) + at, o);
-    if (a.o1 != nullptr) store_row<T, VEC>(static_cast<T*>(a.o1) + at, dg);
+    if (a.o0 != nullptr) store_row_last<T, VEC>(static_cast<T*>(a.o0) + at, o);
+    if (a.o1 != nullptr) store_row_last<T, VEC>(static_cast<T*>(a.o1) + at, dg);
   }
 }
 
@@ -359,20 +411,20 @@ __device__ __forceinline__ void gn_zero_rows(const NormArgs& a, int col, int64_t
   for (int i = 0; i < VEC; ++i) zero.v[i] = T(0);
 #pragma unroll 1
   for (int64_t r = from; r < to; r += step) {
-    if (a.o0 != nullptr) store_row<T, VEC>(static_cast<T*>(a.o0) + r * a.lay.dim + col, zero);
-    if (OP == GN_DBL && a.o1 != nullptr) store_row<T, VEC>(static_cast<T*>(a.o1) + r * a.lay.dim + col, zero);
+    if (a.o0 != nullptr) store_row_last<T, VEC>(static_cast<T*>(a.o0) + r * a.lay.dim + col, zero);
+    if (OP == GN_DBL && a.o1 != nullptr) store_row_last<T, VEC>(static_cast<T*>(a.o1) + r * a.lay.dim + col, zero);
   }
 }
 
-// Column sums of a CTA: thread slots colacc[2 VEC][GN_THREADS] (weights, then biases) added over the row
+// Column sums of a CTA: thread slots colacc[2 VEC][threads] (weights, then biases) added over the row
 // lanes of a column into slot `part` of colpart.  All threads call it.
-template <int VEC>
+template <int VEC, int NT = GN_THREADS>
 __device__ __forceinline__ void gn_store_columns(const NormArgs& a, const double* colacc, int part, int v0, int W,
                                                  int TX, int TY) {
   __syncthreads();
-  for (int q = int(threadIdx.x); q < 2 * VEC * W; q += GN_THREADS) {
+  for (int q = int(threadIdx.x); q < 2 * VEC * W; q += NT) {
     const int which = q / (VEC * W), cc = q % (VEC * W), tx = cc / VEC, i = cc % VEC;
-    const double* p = colacc + (which * VEC + i) * GN_THREADS + tx;
+    const double* p = colacc + (which * VEC + i) * NT + tx;
     double s = 0.0;
     for (int y = 0; y < TY; ++y) s += p[y * TX];
     a.colpart[(2 * int64_t(part) + which) * a.lay.dim + v0 * VEC + cc] = s;
@@ -382,9 +434,9 @@ __device__ __forceinline__ void gn_store_columns(const NormArgs& a, const double
 
 // Gradients of the weights and biases of a tile's channels from the column sums of all `parts` CTAs, after
 // the grid has met; CTA `rank` of `ranks` takes its share.  A tile holds whole channels.
-template <typename T, int VEC>
+template <typename T, int VEC, int NT = GN_THREADS>
 __device__ __forceinline__ void gn_finish_columns(const NormArgs& a, int parts, int v0, int W, int rank, int ranks) {
-  constexpr int WARPS = GN_THREADS / 32;
+  constexpr int WARPS = NT / 32;
   const int lane = int(threadIdx.x) % 32, n = W * VEC;
   for (int q = rank * WARPS + int(threadIdx.x) / 32; q < n; q += ranks * WARPS) {
     const int col = v0 * VEC + q;
@@ -448,7 +500,7 @@ __device__ __forceinline__ void gn_publish(const COL& c, const ACC& acc, T piv, 
       s2 += acc.s2[i];
     }
     if (KIND != GN_PLAIN) {
-      const T n = T(rows * VEC), m = rows > 0 ? s1 / n : T(0);
+      const T n = T(rows * VEC), m = rows > 0 ? s1 * gn_recip(n) : T(0);
       buf[0] = piv;
       buf[stride] = m;
       buf[2 * stride] = s2 - m * s1;
@@ -471,43 +523,65 @@ __device__ __forceinline__ void gn_publish(const COL& c, const ACC& acc, T piv, 
   }
 }
 
+// Sum of v over groups of `lanes` (a power of two) consecutive threads.
+template <typename T>
+__device__ __forceinline__ T gn_lanes_sum(T v, int lanes) {
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) {
+    const T w = __shfl_xor_sync(~0u, v, o);
+    v += o < lanes ? w : T(0);
+  }
+  return v;
+}
+
 // Join E entries: `lanes` consecutive threads share them, entry i's sums are at(i)[0], at(i)[stride], ..; every
-// thread of the warp calls it.  All of the lanes get S.
-template <int OP, typename T, typename F>
+// thread of the warp calls it.  All of the lanes get S.  This sits between two barriers, so what counts
+// is the length of its chain of dependent instructions: a lane keeps its first CACHE entries in registers.
+template <int OP, typename T, int CACHE = 1, typename F>
 __device__ __forceinline__ void gn_join(int E, int lane, int lanes, int stride, bool scalar, T* S, F at) {
   constexpr int NS = gn_sums(OP);
   if constexpr (OP == GN_FWD) {
     T piv = T(0), mean = T(0), n = T(0), m2 = T(0);
     if (__any_sync(~0u, scalar)) {
-      if (scalar && E > 0) {
-        piv = *at(0);
-#pragma unroll 2
-        for (int i = lane; i < E; i += lanes) {
+      T d[CACHE], cnt[CACHE];
+      if (scalar && E > 0) piv = *at(0);
+#pragma unroll
+      for (int c = 0; c < CACHE; ++c) {
+        d[c] = cnt[c] = T(0);
+        const int i = lane + c * lanes;
+        if (scalar && i < E) {
           const T* p = at(i);
-          const T cnt = p[3 * stride];
-          n += cnt;
-          mean += cnt * ((p[0] - piv) + p[stride]);
+          cnt[c] = p[3 * stride];
+          d[c] = (p[0] - piv) + p[stride];
+          m2 += p[2 * stride];
         }
+        n += cnt[c];
+        mean += cnt[c] * d[c];
       }
-      for (int o = lanes / 2; o > 0; o /= 2) {
-        mean += __shfl_xor_sync(~0u, mean, o);
-        n += __shfl_xor_sync(~0u, n, o);
+      for (int i = lane + CACHE * lanes; scalar && i < E; i += lanes) {
+        const T* p = at(i);
+        const T w = p[3 * stride];
+        n += w;
+        mean += w * ((p[0] - piv) + p[stride]);
       }
-      if (n > T(0)) mean /= n;
+      mean = gn_lanes_sum(mean, lanes);
+      n = gn_lanes_sum(n, lanes);
+      if (n > T(0)) mean *= gn_recip(n);
+#pragma unroll
+      for (int c = 0; c < CACHE; ++c) m2 += cnt[c] * (d[c] - mean) * (d[c] - mean);
+      for (int i = lane + CACHE * lanes; scalar && i < E; i += lanes) {
+        const T* p = at(i);
+        const T e = ((p[0] - piv) + p[stride]) - mean;
+        m2 += p[2 * stride] + p[3 * stride] * e * e;
+      }
     }
-#pragma unroll 2
-    for (int i = lane; i < E; i += lanes) {
-      const T* p = at(i);
-      m2 += p[2 * stride];
-      if (scalar) {
-        const T d = ((p[0] - piv) + p[stride]) - mean;
-        m2 += p[3 * stride] * d * d;
-      }
+    if (!scalar) {
+#pragma unroll 4
+      for (int i = lane; i < E; i += lanes) m2 += at(i)[2 * stride];
     }
-    for (int o = lanes / 2; o > 0; o /= 2) m2 += __shfl_xor_sync(~0u, m2, o);
     S[0] = piv;
     S[1] = mean;
-    S[2] = m2;
+    S[2] = gn_lanes_sum(m2, lanes);
     S[3] = n;
   } else {
 #pragma unroll
@@ -518,48 +592,60 @@ __device__ __forceinline__ void gn_join(int E, int lane, int lanes, int stride, 
 #pragma unroll
       for (int p = 0; p < NS; ++p) S[p] += e[p * stride];
     }
-    for (int o = lanes / 2; o > 0; o /= 2) {
 #pragma unroll
-      for (int p = 0; p < NS; ++p) S[p] += __shfl_xor_sync(~0u, S[p], o);
-    }
+    for (int p = 0; p < NS; ++p) S[p] = gn_lanes_sum(S[p], lanes);
   }
 }
 
 // ------------------------------------------------------------------------------------- local ---
 // Thread (j, k, tx) owns vector column tx of the CTA's tile and row lane k of segments j, j + J, ..
-// (M of them) of the current batch; it keeps R rows of each in registers.  With CL a cluster's CTAs have K
-// row lanes each of one segment; each writes its sums into the shared memory of all.
-template <typename T, int VEC, int OP, int R, int M, bool CL>
+// (M of them) of the current batch; R rows of each wait in its slots, while the next batch is on its
+// way into others.  With CL a cluster's CTAs have K row lanes each of one segment; each writes its
+// sums into the shared memory of all.
+template <typename T, int VEC, int OP, int R, int M, bool CL, int NT>
 struct GnLocal {
   static constexpr int NS = gn_sums(OP), NC = gn_coefs(OP);
-  static constexpr size_t buf_bytes = sizeof(T) * NS * M * GN_THREADS;
-  static constexpr size_t res_bytes = sizeof(T) * NC * M * GN_THREADS;
+  static constexpr size_t slot_bytes = size_t(2) * R * M * GnSlots<T, VEC, OP, NT>::SLOT;
+  static constexpr size_t col_bytes = OP == GN_FWD ? 0 : sizeof(double) * 2 * VEC * NT;
+  static constexpr size_t buf_bytes = sizeof(T) * NS * M * NT;
   // sums of a cluster's CTAs, twice: [parity][sum][rank][local group]
   static constexpr int ALL_GROUPS = 32;
   static constexpr size_t all_bytes = CL ? sizeof(T) * 2 * NS * 16 * ALL_GROUPS : 0;
-  static constexpr size_t col_bytes = OP == GN_FWD ? 0 : sizeof(double) * 2 * VEC * GN_THREADS;
-  static constexpr size_t smem = buf_bytes + res_bytes + all_bytes + col_bytes + sizeof(GnRange) * GN_THREADS;
+  static constexpr size_t fixed = slot_bytes + col_bytes + buf_bytes + all_bytes;
+  // + per item of a batch its coefficients, per group of a tile its range, per segment of two batches its rows
+  static size_t smem(const NormArgs& a) {
+    return fixed + sizeof(T) * NC * M * a.j * a.tile_groups + sizeof(GnRange) * a.tile_groups + 8 * M * a.j;
+  }
 };
 
 // A thread's part of a batch: rows row0[m] + i step, i < n[m].
-template <typename T, int VEC, int R, int M>
+template <int M>
 struct GnBatch {
-  GnRow<T, VEC> v[R * M];
   int row0[M], n[M];
 };
 
-template <int KIND, typename T, int VEC, int OP, bool DROP, int R, int M>
+template <int KIND, typename T, int VEC, int OP, bool DROP, int R, int M, int NT>
 __device__ __forceinline__ void gn_local_sums(const GnCol<T, VEC, OP, DROP>& c, const GnStat<T> (&st)[M],
-                                              GnBatch<T, VEC, R, M>& t, int step, T* buf, T* cw, T* cb) {
+                                              const GnSlots<T, VEC, OP, NT>& sl, int slot0, const GnBatch<M>& t, int step,
+                                              T* buf, T* cw, T* cb) {
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     GnAcc<T, VEC, OP, DROP> acc;
     acc.clear(c);
-    const T piv = OP == GN_FWD && KIND != GN_PLAIN && t.n[m] > 0 ? t.v[m * R].x.v[0] : T(0);
+    T piv = T(0);
 #pragma unroll
     for (int i = 0; i < R; ++i)
-      if (i < t.n[m]) acc.template add<KIND>(c, st[m], piv, t.v[m * R + i], t.row0[m] + i * step);
-    gn_publish<KIND, OP, T, VEC>(c, acc, piv, t.n[m], buf + m * GN_THREADS, M * GN_THREADS);
+      if (i < t.n[m]) {
+        GnRow<T, VEC> v;
+        sl.read(slot0 + m * R + i, v);
+        if (OP == GN_FWD && KIND != GN_PLAIN && i == 0) piv = v.x.v[0];
+        acc.template add<KIND>(c, st[m], piv, v, t.row0[m] + i * step);
+        if (OP == GN_BWD) {  // z and c for the second pass
+          sl.write(slot0 + m * R + i, 0, v.x);
+          sl.write(slot0 + m * R + i, 1, v.g);
+        }
+      }
+    gn_publish<KIND, OP, T, VEC>(c, acc, piv, t.n[m], buf + m * NT, M * NT);
     if constexpr (OP == GN_BWD) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
@@ -570,10 +656,11 @@ __device__ __forceinline__ void gn_local_sums(const GnCol<T, VEC, OP, DROP>& c, 
   }
 }
 
-template <int KIND, typename T, int VEC, int OP, bool DROP, int R, int M>
+template <int KIND, typename T, int VEC, int OP, bool DROP, int R, int M, int NT>
 __device__ __forceinline__ void gn_local_apply(const NormArgs& a, const GnCol<T, VEC, OP, DROP>& c,
-                                               GnStat<T> (&st)[M], GnBatch<T, VEC, R, M>& t, int step, const T* res,
-                                               int res_step, T* cw, T* cb) {
+                                               GnStat<T> (&st)[M], const GnSlots<T, VEC, OP, NT>& sl, int slot0,
+                                               const GnBatch<M>& t, int step, const T* res, int res_step, T* cw,
+                                               T* cb) {
   constexpr int NC = gn_coefs(OP);
 #pragma unroll
   for (int m = 0; m < M; ++m) {
@@ -589,25 +676,31 @@ __device__ __forceinline__ void gn_local_apply(const NormArgs& a, const GnCol<T,
     for (int i = 0; i < R; ++i)
       if (i < t.n[m]) {
         const int r = t.row0[m] + i * step;
-        gn_apply<KIND>(a, c, st[m], kf, t.v[m * R + i], int64_t(r) * a.lay.dim + c.col, r, cw, cb);
+        GnRow<T, VEC> v;
+        sl.read(slot0 + m * R + i, v);
+        gn_apply<KIND>(a, c, st[m], kf, v, int64_t(r) * a.lay.dim + c.col, r, cw, cb);
       }
   }
 }
 
-// CTAs that have to fit an SM: what the registers of a batch allow
-__host__ __device__ constexpr int gn_local_ctas(int op, int m) { return op == GN_FWD ? 3 : m > 1 ? 3 : 2; }
+// CTAs that have to fit an SM
+__host__ __device__ constexpr int gn_local_ctas(int op, int threads) {
+  return threads > GN_THREADS ? (op == GN_FWD ? 2 : 1) : op == GN_DBL ? 2 : 3;
+}
 
-template <typename T, int VEC, int OP, bool DROP, int R, int M, bool CL>
-__global__ void __launch_bounds__(GN_THREADS, gn_local_ctas(OP, M))
+template <typename T, int VEC, int OP, bool DROP, int R, int M, bool CL, int NT>
+__global__ void __launch_bounds__(NT, gn_local_ctas(OP, NT))
 gn_local_kernel(const __grid_constant__ NormArgs a) {
-  using L = GnLocal<T, VEC, OP, R, M, CL>;
-  constexpr int NS = L::NS, NC = L::NC, STRIDE = M * GN_THREADS;
+  using L = GnLocal<T, VEC, OP, R, M, CL, NT>;
+  constexpr int NS = L::NS, NC = L::NC, STRIDE = M * NT;
   extern __shared__ __align__(16) unsigned char smem[];
-  double* colbase = reinterpret_cast<double*>(smem);
-  T* buf = reinterpret_cast<T*>(smem + L::col_bytes);
-  T* res = buf + NS * STRIDE;
-  T* all = res + NC * STRIDE;
-  GnRange* gs = reinterpret_cast<GnRange*>(smem + L::col_bytes + L::buf_bytes + L::res_bytes + L::all_bytes);
+  unsigned char* sp = smem + L::slot_bytes;
+  double* colbase = reinterpret_cast<double*>(sp);
+  T* buf = reinterpret_cast<T*>(sp + L::col_bytes);
+  T* all = buf + NS * STRIDE;
+  T* res = reinterpret_cast<T*>(sp + L::col_bytes + L::buf_bytes + L::all_bytes);
+  GnRange* gs = reinterpret_cast<GnRange*>(res + NC * M * a.j * a.tile_groups);
+  int* lens = reinterpret_cast<int*>(gs + a.tile_groups);  // rows of a batch's segments: [parity][M J]
   const int CS = CL ? a.cs : 1, rank = CL ? int(blockIdx.x) % CS : 0;
   const int part = CL ? int(blockIdx.x) / CS : int(blockIdx.x), parts = CL ? int(gridDim.x) / CS : int(gridDim.x);
   const int tid = int(threadIdx.x), tx = tid % a.tx, ty = tid / a.tx;
@@ -617,38 +710,54 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
   const bool active = tx < W && j < J;
   const int64_t G = a.lay.n_groups();
 
-  GnCol<T, VEC, OP, DROP> c;
-  c.col = (v0 + (active ? tx : 0)) * VEC;
-  GnBatch<T, VEC, R, M> t;
+  GnSlots<T, VEC, OP, NT> sl;
+  sl.init(a, smem);
+  const int col = (v0 + (active ? tx : 0)) * VEC;
   const uint32_t div_step = step > 1 ? 0xFFFFFFFFu / uint32_t(step) + 1u : 0u;
-  // rows of the batch of segments b0 .. and their loads
-  auto fetch = [&](int64_t b0) {
+  const int64_t hop_b = int64_t(parts) * (J * M);
+  int lo[M], hi[M];  // row pointers of the batch after the one on its way
+  auto point = [&](int64_t b0) {
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      t.n[m] = 0;
+      lo[m] = hi[m] = 0;
       const int64_t b = b0 + m * J + j;
       if (active && b < a.B) {
-        int s, e;
-        gn_segment(a, int(b), s, e);
-        if (e - s > R * step) {  // longer than the caller said
-          atomicCAS(a.status, 0, int(E3_ERR_INDEX));
-          e = s + R * step;
-        }
-        t.row0[m] = s + k;
-        const int left = e - s - k + step - 1;
-        t.n[m] = left > 0 ? (R == 1 ? (e > s + k) : int(fast_div(uint32_t(left), div_step))) : 0;
+        lo[m] = a.row_ptr != nullptr ? a.row_ptr[b] : 0;
+        hi[m] = a.row_ptr != nullptr ? a.row_ptr[b + 1] : int(a.N);
+        if (b == 0 && lo[m] != 0) hi[m] = -1;  // reported below
       }
+    }
+  };
+  // rows of the batch that lo and hi point to, on their way into the slots of parity `half`
+  auto fetch = [&](int half, GnBatch<M>& t) {
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      int s = lo[m], e = hi[m];
+      if (s < 0 || e < s || e > int(a.N) || e - s > R * step) {  // no row pointer, or longer than the caller said
+        atomicCAS(a.status, 0, int(E3_ERR_INDEX));
+        s = min(max(s, 0), int(a.N));
+        e = min(min(max(e, s), int(a.N)), s + R * step);
+      }
+      t.row0[m] = s + k;
+      const int left = e - s - k + step - 1;
+      t.n[m] = !active ? 0 : R == 1 ? int(e > s + k) : left > 0 ? int(fast_div(uint32_t(left), div_step)) : 0;
+      if (active && tx == 0 && ty == j * K) lens[(half * M + m) * J + j] = e - s;
     }
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
       for (int i = 0; i < R; ++i)
         if (i < t.n[m])
-          gn_load<T, VEC, OP>(a, int64_t(t.row0[m] + i * step) * a.lay.dim + c.col, t.v[m * R + i]);
+          sl.fetch((half * M + m) * R + i, (int64_t(t.row0[m] + i * step) * a.lay.dim + col) * int64_t(sizeof(T)));
+    sl.commit();
   };
   int64_t b0 = int64_t(part) * (J * M);
-  fetch(b0);
+  GnBatch<M> t;
+  point(b0);
+  fetch(0, t);
+  point(b0 + hop_b);
 
+  GnCol<T, VEC, OP, DROP> c;
   c.init(a, v0, W, active ? tx : 0);
   const int gfirst = c.g - c.lg, nlg = group_of(a.lay, (v0 + W) * VEC - 1) - gfirst + 1;
   if (active && ty == 0 && tx == c.g0) gs[c.lg] = gn_range(c.g0, c.g1);
@@ -658,15 +767,19 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
   for (int i = 0; i < VEC; ++i) cw[i] = cb[i] = T(0);
   if (columns) {
 #pragma unroll
-    for (int i = 0; i < 2 * VEC; ++i) colbase[i * GN_THREADS + tid] = 0.0;
+    for (int i = 0; i < 2 * VEC; ++i) colbase[i * NT + tid] = 0.0;
   }
   const uint32_t div_nlg = nlg > 1 ? 0xFFFFFFFFu / uint32_t(nlg) + 1u : 0u;
   const uint32_t div_j = J > 1 ? 0xFFFFFFFFu / uint32_t(J) + 1u : 0u;
-  const int lane = tid & (a.lanes - 1), sub = tid / a.lanes, per = GN_THREADS / a.lanes;
+  const int lane = tid & (a.lanes - 1), sub = tid / a.lanes, per = NT / a.lanes;
   const int items = M * J * nlg;
   int rows_held = 0, parity = 0;
   if (CL) cooperative_groups::this_cluster().sync();  // every CTA of the cluster has started
-  for (; b0 < a.B; parity ^= 1) {
+  for (; b0 < a.B; b0 += hop_b, parity ^= 1) {
+    GnBatch<M> next;
+    fetch(parity ^ 1, next);
+    point(b0 + 2 * hop_b);
+    const int slot0 = parity * R * M;
     GnStat<T> st[M];
     if (OP != GN_FWD) {
 #pragma unroll
@@ -675,9 +788,11 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
         if (t.n[m] > 0) st[m].set(a.stats + 2 * (b * G + c.g));
       }
     }
-    if (c.kind == GN_PLAIN) gn_local_sums<GN_PLAIN>(c, st, t, step, buf + tid, cw, cb);
-    else if (c.kind == GN_CENTRED) gn_local_sums<GN_CENTRED>(c, st, t, step, buf + tid, cw, cb);
-    else gn_local_sums<GN_ACT>(c, st, t, step, buf + tid, cw, cb);
+    sl.template wait<1>();
+    if (c.kind == GN_PLAIN) gn_local_sums<GN_PLAIN, T, VEC, OP, DROP, R, M, NT>(c, st, sl, slot0, t, step, buf + tid, cw, cb);
+    else if (c.kind == GN_CENTRED)
+      gn_local_sums<GN_CENTRED, T, VEC, OP, DROP, R, M, NT>(c, st, sl, slot0, t, step, buf + tid, cw, cb);
+    else gn_local_sums<GN_ACT, T, VEC, OP, DROP, R, M, NT>(c, st, sl, slot0, t, step, buf + tid, cw, cb);
     __syncthreads();
     // item (m, jj, lg): K row lanes x the group's vectors
     for (int base = 0; base < items; base += per) {
@@ -690,7 +805,7 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
       const bool scalar = blk.bias0 >= 0;
       GnRange gr{0, 1, 0};
       if (ok) gr = gs[lg];
-      const T* q = buf + m * GN_THREADS + jj * K * a.tx + gr.first;
+      const T* q = buf + m * NT + jj * K * a.tx + gr.first;
       const int hop = a.tx - gr.w;
       T S[NS];
       gn_join<OP, T>(ok ? K * gr.w : 0, lane, a.lanes, STRIDE, scalar, S,
@@ -706,15 +821,13 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
           }
         }
       } else if (ok && lane == 0) {
-        int s = 0, e = int(a.N);
-        if (a.row_ptr != nullptr) gn_segment(a, int(b), s, e);
-        gn_finish<OP, T>(S, T(e - s) * T(blk.group_cols), scalar, a.stats + 2 * (b * G + g), true, a.eps,
-                         res + NC * it);
+        const T r = OP == GN_DBL ? T(a.stats[2 * (b * G + g) + 1]) : T(0);
+        gn_finish<OP, T>(S, T(lens[parity * M * J + mj]) * T(blk.group_cols), scalar, r, T(a.eps), res + NC * it);
       }
     }
     if (CL) {
       cooperative_groups::this_cluster().sync();
-      for (int base = 0; base < nlg; base += GN_THREADS / 16) {
+      for (int base = 0; base < nlg; base += NT / 16) {
         const int lg = base + tid / 16, g = gfirst + (lg < nlg ? lg : 0);
         const RowBlock& blk = a.lay.blk[fast_div(uint32_t(g), a.lay.div_groups)];
         const bool scalar = blk.bias0 >= 0;
@@ -723,55 +836,61 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
         gn_join<OP, T>(lg < nlg ? CS : 0, tid % 16, 16, 16 * L::ALL_GROUPS, scalar, S,
                        [&](int i) { return q + i * L::ALL_GROUPS; });
         if (lg < nlg && tid % 16 == 0) {
-          int s = 0, e = int(a.N);
-          if (a.row_ptr != nullptr) gn_segment(a, int(b0), s, e);
-          gn_finish<OP, T>(S, T(e - s) * T(blk.group_cols), scalar, a.stats + 2 * (b0 * G + g), rank == 0, a.eps,
-                           res + NC * lg);
+          const T r = OP == GN_DBL ? T(a.stats[2 * (b0 * G + g) + 1]) : T(0);
+          gn_finish<OP, T>(S, T(lens[parity]) * T(blk.group_cols), scalar, r, T(a.eps), res + NC * lg);
         }
       }
     }
     __syncthreads();
-    {
-      const T* q = res + NC * ((active ? j : 0) * nlg + c.lg);
-      const int res_step = NC * J * nlg;
-      if (c.kind == GN_PLAIN) gn_local_apply<GN_PLAIN>(a, c, st, t, step, q, res_step, cw, cb);
-      else if (c.kind == GN_CENTRED) gn_local_apply<GN_CENTRED>(a, c, st, t, step, q, res_step, cw, cb);
-      else gn_local_apply<GN_ACT>(a, c, st, t, step, q, res_step, cw, cb);
+    if (OP == GN_FWD && rank == 0) {
+      for (int it = tid; it < items; it += NT) {
+        const int mj = int(fast_div(uint32_t(it), div_nlg)), lg = it - mj * nlg;
+        if (b0 + mj < a.B) gn_store_stats(res + NC * it, a.stats + 2 * ((b0 + mj) * G + gfirst + lg));
+      }
     }
+    const T* q = res + NC * ((active ? j : 0) * nlg + c.lg);
+    const int hop_res = NC * J * nlg;
+    if (c.kind == GN_PLAIN)
+      gn_local_apply<GN_PLAIN, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, slot0, t, step, q, hop_res, cw, cb);
+    else if (c.kind == GN_CENTRED)
+      gn_local_apply<GN_CENTRED, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, slot0, t, step, q, hop_res, cw, cb);
+    else gn_local_apply<GN_ACT, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, slot0, t, step, q, hop_res, cw, cb);
     rows_held += R * M;
     if (columns && rows_held >= GN_FLUSH) {
       rows_held = 0;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        colbase[i * GN_THREADS + tid] += double(cw[i]);
-        colbase[(VEC + i) * GN_THREADS + tid] += double(cb[i]);
+        colbase[i * NT + tid] += double(cw[i]);
+        colbase[(VEC + i) * NT + tid] += double(cb[i]);
         cw[i] = cb[i] = T(0);
       }
     }
-    b0 += int64_t(parts) * (J * M);
-    fetch(b0);
+    t = next;
   }
+  sl.template wait<0>();
   if (active)
     gn_zero_rows<T, VEC, OP>(a, c.col, gn_rows_end(a) + int64_t(blockIdx.x) * (J * K) + ty, a.N,
                              int64_t(gridDim.x) * (J * K));
   if (columns) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      colbase[i * GN_THREADS + tid] += double(cw[i]);
-      colbase[(VEC + i) * GN_THREADS + tid] += double(cb[i]);
+      colbase[i * NT + tid] += double(cw[i]);
+      colbase[(VEC + i) * NT + tid] += double(cb[i]);
     }
-    gn_store_columns<VEC>(a, colbase, int(blockIdx.x), v0, W, a.tx, J * K);
+    gn_store_columns<VEC, NT>(a, colbase, int(blockIdx.x), v0, W, a.tx, J * K);
     cooperative_groups::this_grid().sync();
-    gn_finish_columns<T, VEC>(a, int(gridDim.x), v0, W, int(blockIdx.x), int(gridDim.x));
+    gn_finish_columns<T, VEC, NT>(a, int(gridDim.x), v0, W, int(blockIdx.x), int(gridDim.x));
   }
 }
 
 // -------------------------------------------------------------------------------------- grid ---
-// CTA (rc, ct): row chunk rc, column tile s cx + ct of slab s.  A segment that lies in one chunk is
+// CTA (rc, ct): row chunk rc, column tile ct; all CTAs are resident.  A segment that lies in one chunk is
 // finished there (unless its group is cut into tiles); the others leave partial sums:
 //   slot of (chunk, segment), part of (tile, group):  part[slot][groups + tiles][sums]
 // slots: 2 chunk (the segment began earlier) or 2 chunk + 1 (it begins here and goes on); with cut
 // groups chunk + segment, which rises by one from piece to piece.  Parts likewise are group + tile.
+// The grid meets, the CTAs that hold a segment share the joining of its groups, the grid meets again, and
+// every CTA reads its rows a second time, from the last one back: those are still in L2.
 template <int OP, typename T>
 __device__ __forceinline__ T* gn_slot(const NormArgs& a, int chunk, int64_t b, bool begins, int tile, int g) {
   const int64_t G = a.lay.n_groups();
@@ -794,27 +913,83 @@ __device__ __forceinline__ int gn_first_segment(const NormArgs& a, int r) {
 template <typename T, int VEC, int OP>
 struct GnGrid {
   static constexpr int NS = gn_sums(OP), NC = gn_coefs(OP);
-  static constexpr int U = OP == GN_FWD ? 8 : OP == GN_BWD ? 4 : 2;  // rows in flight per thread
+  static constexpr int U = OP == GN_FWD ? 4 : OP == GN_BWD ? 2 : 1;  // rows that a thread takes at a time
+  static constexpr int STAGES = 4;                                   // such groups in flight
+  static constexpr size_t slot_bytes = size_t(STAGES) * U * GnSlots<T, VEC, OP>::SLOT;
   static constexpr size_t long_bytes = OP == GN_DBL ? sizeof(double) * NS * GN_THREADS : 0;
   static constexpr size_t buf_bytes = sizeof(T) * NS * GN_THREADS;
-  static constexpr size_t res_bytes = sizeof(T) * NC * GN_THREADS;
   static constexpr size_t col_bytes = OP == GN_FWD ? 0 : sizeof(double) * 2 * VEC * GN_THREADS;
-  static constexpr size_t smem = long_bytes + col_bytes + buf_bytes + res_bytes + sizeof(GnRange) * GN_THREADS;
-};
-struct GnGridSmem {
-  double *sums, *columns;  // a thread's long sums (double backward) and column sums
-  void *buf, *res;
-  GnRange* gs;
+  static constexpr size_t smem = slot_bytes + long_bytes + col_bytes + buf_bytes + sizeof(GnRange) * GN_THREADS;
 };
 
-// A thread's sums over rows s + ty, s + ty + K, .. of a piece into its slots of buf (and of the columns).
+// A thread's rows of a piece, in order or backwards, through a ring of slots.
+template <typename T, int VEC, int OP>
+struct GnStream {
+  static constexpr int U = GnGrid<T, VEC, OP>::U, STAGES = GnGrid<T, VEC, OP>::STAGES;
+  GnSlots<T, VEC, OP> sl;
+  int64_t at, step;  // bytes: the next row to fetch, the way from a row to the next
+  int left;          // rows still to fetch
+  int put, take;     // ring positions
+
+  __device__ __forceinline__ void issue() {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (i < left) {
+        sl.fetch(put * U + i, at);
+        at += step;
+      }
+    left -= U;
+    put = (put + 1) % STAGES;
+    sl.commit();
+  }
+  // n rows from row r0 on, every K-th; `back`: from the last one down
+  __device__ __forceinline__ void start(const NormArgs& a, int col, int r0, int n, int K, bool back) {
+    const int64_t row = int64_t(a.lay.dim) * sizeof(T);
+    step = back ? -K * row : K * row;
+    at = (back ? int64_t(r0) + int64_t(n - 1) * K : int64_t(r0)) * row + col * int64_t(sizeof(T));
+    left = n;
+    put = take = 0;
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) issue();
+  }
+  // f(i, row's vectors) for the rows of the next group that are there
+  template <typename F>
+  __device__ __forceinline__ void next(int n, F f) {
+    sl.template wait<STAGES - 2>();
+    GnRow<T, VEC> v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) sl.read(take * U + i, v[i]);
+    issue();  // into the slots read in the step before
+    take = (take + 1) % STAGES;
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (i < n) f(i, v[i]);
+  }
+};
+
+// The pieces (segment x chunk) of a chunk of rows, in order.
+struct GnPiece {
+  int b, s, e, ps, pe;  // segment, its rows, the rows in the chunk
+  __device__ __forceinline__ bool next(const NormArgs& a, int lo, int hi) {
+    for (++b; b < a.B; ++b) {
+      gn_segment(a, b, s, e);
+      if (s >= hi) return false;
+      ps = max(s, lo);
+      pe = min(e, hi);
+      if (ps < pe) return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ bool whole(const NormArgs& a) const { return ps == s && pe == e && !a.wide; }
+};
+
+// A thread's sums over the rows of a stream into its slots of buf (and of the columns).
 template <int KIND, typename T, int VEC, int OP, bool DROP>
 __device__ __forceinline__ void gn_grid_sums(const NormArgs& a, const GnCol<T, VEC, OP, DROP>& c, const GnStat<T>& st,
-                                             int s, int e, int ty, int K, T* buf, double* sums, double* colacc) {
+                                             GnStream<T, VEC, OP>& q, int r0, int n, int K, T* buf, double* sums,
+                                             double* colacc) {
   constexpr int U = GnGrid<T, VEC, OP>::U;
-  const int64_t D = a.lay.dim;
   T piv = T(0);
-  if (OP == GN_FWD && KIND != GN_PLAIN && s + ty < e) piv = static_cast<const T*>(a.x)[(s + ty) * D + c.col];
   GnAcc<T, VEC, OP, DROP> acc;
   acc.clear(c);
   double l1 = 0.0, l2 = 0.0;  // the sums of earlier flushes
@@ -823,25 +998,20 @@ __device__ __forceinline__ void gn_grid_sums(const NormArgs& a, const GnCol<T, V
     for (int i = 0; i < 12; ++i) sums[i * GN_THREADS] = 0.0;
   }
 #pragma unroll 1
-  for (int f = s + ty; f < e; f += K * GN_FLUSH) {
-    const int fe = min(e, f + K * GN_FLUSH);
+  for (int f = 0; f < n; f += GN_FLUSH) {
+    const int fe = min(n, f + GN_FLUSH);
 #pragma unroll 1
-    for (int r = f; r < fe; r += K * U) {
-      GnRow<T, VEC> v[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i)  // past the end: the last row again
-        gn_load<T, VEC, OP>(a, min(r + i * K, fe - 1) * D + c.col, v[i]);
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (r + i * K < fe) acc.template add<KIND>(c, st, piv, v[i], r + i * K);
-    }
+    for (int r = f; r < fe; r += U)
+      q.next(fe - r, [&](int i, GnRow<T, VEC>& v) {
+        if (OP == GN_FWD && KIND != GN_PLAIN && r + i == 0) piv = v.x.v[0];
+        acc.template add<KIND>(c, st, piv, v, r0 + (r + i) * K);
+      });
     if constexpr (OP == GN_FWD) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         l1 += double(acc.s1[i]);
         l2 += double(acc.s2[i]);
       }
-      acc.clear(c);
     } else if constexpr (OP == GN_BWD) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
@@ -852,20 +1022,18 @@ __device__ __forceinline__ void gn_grid_sums(const NormArgs& a, const GnCol<T, V
           if (KIND != GN_PLAIN) colacc[(VEC + i) * GN_THREADS] += double(acc.s2[i]);
         }
       }
-      acc.clear(c);
     } else {
 #pragma unroll
       for (int i = 0; i < 12; ++i) sums[i * GN_THREADS] += double(acc.s[i]);
-      acc.clear(c);
     }
+    acc.clear(c);
   }
   if constexpr (OP == GN_FWD) {
-    const int rows = s + ty < e ? (e - s - ty + K - 1) / K : 0;
-    const double n = double(rows) * VEC, m = KIND != GN_PLAIN && rows > 0 ? l1 / n : 0.0;
+    const double cnt = double(n) * VEC, m = KIND != GN_PLAIN && n > 0 ? l1 / cnt : 0.0;
     buf[0] = piv;
     buf[GN_THREADS] = T(m);
     buf[2 * GN_THREADS] = T(l2 - m * l1);
-    buf[3 * GN_THREADS] = T(n);
+    buf[3 * GN_THREADS] = T(cnt);
   } else if constexpr (OP == GN_BWD) {
     buf[0] = T(l1);
     buf[GN_THREADS] = T(l2);
@@ -875,33 +1043,31 @@ __device__ __forceinline__ void gn_grid_sums(const NormArgs& a, const GnCol<T, V
   }
 }
 
+// Pointwise results of the rows of a stream that runs backwards from row r0 + (n - 1) K.
 template <int KIND, typename T, int VEC, int OP, bool DROP>
 __device__ __forceinline__ void gn_grid_apply(const NormArgs& a, const GnCol<T, VEC, OP, DROP>& c, const GnStat<T>& st,
-                                              const T* kf, int s, int e, int ty, int K, double* colacc) {
+                                              const T* kf, GnStream<T, VEC, OP>& q, int r0, int n, int K,
+                                              double* colacc) {
   constexpr int U = GnGrid<T, VEC, OP>::U;
   const int64_t D = a.lay.dim;
-  if (OP == GN_BWD && a.o0 == nullptr) return;
+  int row = r0 + (n - 1) * K;
 #pragma unroll 1
-  for (int f = s + ty; f < e; f += K * GN_FLUSH) {
-    const int fe = min(e, f + K * GN_FLUSH);
+  for (int f = 0; f < n; f += GN_FLUSH) {
+    const int fe = min(n, f + GN_FLUSH);
     T cw[VEC], cb[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) cw[i] = cb[i] = T(0);
 #pragma unroll 1
-    for (int r = f; r < fe; r += K * U) {
-      GnRow<T, VEC> v[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i) gn_load<T, VEC, OP>(a, min(r + i * K, fe - 1) * D + c.col, v[i]);
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (r + i * K < fe) {
-          if constexpr (OP == GN_BWD) {  // z and c again
-            GnAcc<T, VEC, OP, DROP> z;
-            z.clear(c);
-            z.template add<KIND>(c, st, T(0), v[i], r + i * K);
-          }
-          gn_apply<KIND>(a, c, st, kf, v[i], (r + i * K) * D + c.col, r + i * K, cw, cb);
+    for (int r = f; r < fe; r += U) {
+      q.next(fe - r, [&](int i, GnRow<T, VEC>& v) {
+        if constexpr (OP == GN_BWD) {  // z and c again
+          GnAcc<T, VEC, OP, DROP> z;
+          z.clear(c);
+          z.template add<KIND>(c, st, T(0), v, row - i * K);
         }
+        gn_apply<KIND>(a, c, st, kf, v, (row - i * K) * D + c.col, row - i * K, cw, cb);
+      });
+      row -= U * K;
     }
     if (OP == GN_DBL && colacc != nullptr) {
 #pragma unroll
@@ -913,184 +1079,152 @@ __device__ __forceinline__ void gn_grid_apply(const NormArgs& a, const GnCol<T, 
   }
 }
 
-// First pass over rows [lo, hi) of a tile.
 template <typename T, int VEC, int OP, bool DROP>
-__device__ __forceinline__ void gn_grid_first(const NormArgs& a, const GnTile& tl, int rc, int lo, int hi,
-                                              const GnGridSmem& sm) {
-  constexpr int NS = gn_sums(OP), NC = gn_coefs(OP);
-  const int tid = int(threadIdx.x), tx = tid % a.tx, ty = tid / a.tx;
+__global__ void __launch_bounds__(GN_THREADS, OP == GN_FWD ? 3 : 2) gn_grid_kernel(const __grid_constant__ NormArgs a) {
+  using L = GnGrid<T, VEC, OP>;
+  constexpr int NS = L::NS, NC = L::NC;
+  extern __shared__ __align__(16) unsigned char smem[];
+  double* sums = reinterpret_cast<double*>(smem + L::slot_bytes);     // a thread's long sums (double backward)
+  double* columns = reinterpret_cast<double*>(smem + L::slot_bytes + L::long_bytes);
+  T* buf = reinterpret_cast<T*>(smem + L::slot_bytes + L::long_bytes + L::col_bytes);
+  GnRange* gs = reinterpret_cast<GnRange*>(smem + L::slot_bytes + L::long_bytes + L::col_bytes + L::buf_bytes);
+  const int rc = int(blockIdx.x) / a.n_tiles, tile = int(blockIdx.x) % a.n_tiles;
+  const int lo = int(min(a.N, rc * a.rows_cta)), hi = int(min(a.N, (rc + 1) * a.rows_cta));
+  const int tid = int(threadIdx.x), tx = tid % a.tx, ty = tid / a.tx, K = a.k;
+  const int v0 = a.tile[tile], W = a.tile[tile + 1] - v0;
+  const bool active = tx < W && ty < K;
   const int64_t G = a.lay.n_groups();
-  const bool active = tx < tl.W && ty < a.k;
-  T* buf = static_cast<T*>(sm.buf);
+
+  GnStream<T, VEC, OP> q;
+  q.sl.init(a, smem);
+  const int first = gn_first_segment(a, lo) - 1;
+  GnPiece p;
+  int n = 0;  // this thread's rows of the piece
+  auto open = [&](bool back) {
+    const bool there = p.next(a, lo, hi);
+    n = there && active && p.ps + ty < p.pe ? (p.pe - p.ps - ty + K - 1) / K : 0;
+    if (OP == GN_BWD && back && a.o0 == nullptr) n = 0;
+    q.start(a, (v0 + tx) * VEC, p.ps + ty, n, K, back);
+    return there;
+  };
+  p.b = first;
+  bool there = open(false);
   GnCol<T, VEC, OP, DROP> c;
-  c.init(a, tl.v0, tl.W, active ? tx : 0);
-  __syncthreads();
-  if (active && ty == 0 && tx == c.g0) sm.gs[c.lg] = gn_range(c.g0, c.g1);
-  double* colacc = nullptr;
-  if (OP == GN_BWD && a.colpart != nullptr) {
-    colacc = sm.columns + tid;
+  c.init(a, v0, W, active ? tx : 0);
+  const int gfirst = c.g - c.lg, nlg = group_of(a.lay, (v0 + W) * VEC - 1) - gfirst + 1;
+  if (active && ty == 0 && tx == c.g0) gs[c.lg] = gn_range(c.g0, c.g1);
+  const bool col_sums = OP != GN_FWD && a.colpart != nullptr;
+  double* colacc = col_sums ? columns + tid : nullptr;
+  if (col_sums) {
 #pragma unroll
     for (int i = 0; i < 2 * VEC; ++i) colacc[i * GN_THREADS] = 0.0;
   }
+  // where the second pass finds the result of (segment b, group g)
+  auto keep = [&](const T* o, int b, int g) {
+    if (OP == GN_FWD) {
+      gn_store_stats(o, a.stats + 2 * (b * G + g));
+    } else {
+      T* dst = static_cast<T*>(a.coef) + NC * (b * G + g);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) dst[i] = o[i];
+    }
+  };
+
+  // first pass
   const int lane = tid & (a.lanes - 1), sub = tid / a.lanes, per = GN_THREADS / a.lanes;
 #pragma unroll 1
-  for (int b = gn_first_segment(a, lo); b < a.B; ++b) {
-    int s, e;
-    gn_segment(a, b, s, e);
-    if (s >= hi) break;
-    const int ps = max(s, lo), pe = min(e, hi);
-    if (ps >= pe) continue;
-    if (active) {
-      GnStat<T> st;
-      if (OP != GN_FWD) st.set(a.stats + 2 * (b * G + c.g));
-      if (c.kind == GN_PLAIN)
-        gn_grid_sums<GN_PLAIN>(a, c, st, ps, pe, ty, a.k, buf + tid, sm.sums + tid, colacc);
-      else if (c.kind == GN_CENTRED)
-        gn_grid_sums<GN_CENTRED>(a, c, st, ps, pe, ty, a.k, buf + tid, sm.sums + tid, colacc);
-      else gn_grid_sums<GN_ACT>(a, c, st, ps, pe, ty, a.k, buf + tid, sm.sums + tid, colacc);
-    }
+  for (; there; there = open(false)) {
+    GnStat<T> st;
+    if (OP != GN_FWD) st.set(a.stats + 2 * (p.b * G + c.g));
+    double* acc = OP == GN_BWD ? colacc : nullptr;
+    if (c.kind == GN_PLAIN) gn_grid_sums<GN_PLAIN>(a, c, st, q, p.ps + ty, n, K, buf + tid, sums + tid, acc);
+    else if (c.kind == GN_CENTRED)
+      gn_grid_sums<GN_CENTRED>(a, c, st, q, p.ps + ty, n, K, buf + tid, sums + tid, acc);
+    else gn_grid_sums<GN_ACT>(a, c, st, q, p.ps + ty, n, K, buf + tid, sums + tid, acc);
     __syncthreads();
-    const bool whole = ps == s && pe == e && !a.wide;
-    for (int base = 0; base < tl.nlg; base += per) {
-      const int lg = base + sub, g = tl.gfirst + (lg < tl.nlg ? lg : 0);
+    for (int base = 0; base < nlg; base += per) {
+      const int lg = base + sub, g = gfirst + (lg < nlg ? lg : 0);
       const RowBlock& blk = a.lay.blk[fast_div(uint32_t(g), a.lay.div_groups)];
       const bool scalar = blk.bias0 >= 0;
       GnRange gr{0, 1, 0};
-      if (lg < tl.nlg) gr = sm.gs[lg];
+      if (lg < nlg) gr = gs[lg];
       T S[NS];
-      gn_join<OP, T>(lg < tl.nlg ? a.k * gr.w : 0, lane, a.lanes, GN_THREADS, scalar, S, [&](int i) {
+      gn_join<OP, T>(lg < nlg ? K * gr.w : 0, lane, a.lanes, GN_THREADS, scalar, S, [&](int i) {
         const int kk = int(fast_div(uint32_t(i), gr.div_w));
         return buf + kk * a.tx + gr.first + i - kk * gr.w;
       });
-      if (lg < tl.nlg && lane == 0) {
-        if (whole) {
+      if (lg < nlg && lane == 0) {
+        if (p.whole(a)) {
           T o[NC];
-          gn_finish<OP, T>(S, T(e - s) * T(blk.group_cols), scalar, a.stats + 2 * (b * G + g), true, a.eps, o);
-          if (OP != GN_FWD) {
-            T* dst = static_cast<T*>(a.coef) + NC * (b * G + g);
-#pragma unroll
-            for (int p = 0; p < NC; ++p) dst[p] = o[p];
-          }
+          const T r = OP == GN_DBL ? T(a.stats[2 * (p.b * G + g) + 1]) : T(0);
+          gn_finish<OP, T>(S, T(p.e - p.s) * T(blk.group_cols), scalar, r, T(a.eps), o);
+          keep(o, p.b, g);
         } else {
-          T* dst = gn_slot<OP, T>(a, rc, b, s >= lo, tl.t, g);
+          T* dst = gn_slot<OP, T>(a, rc, p.b, p.s >= lo, tile, g);
 #pragma unroll
-          for (int p = 0; p < NS; ++p) dst[p] = S[p];
+          for (int i = 0; i < NS; ++i) dst[i] = S[i];
         }
       }
     }
     __syncthreads();
   }
-  if (OP == GN_BWD && a.colpart != nullptr) gn_store_columns<VEC>(a, sm.columns, rc, tl.v0, tl.W, a.tx, a.k);
-}
-
-// res[lg] = coefficients of segment b (rows [s, e)), whose sums are spread over chunks and tiles.
-template <int VEC, int OP, typename T>
-__device__ __forceinline__ void gn_grid_join(const NormArgs& a, const GnTile& tl, int rc, int b, int s, int e, T* res) {
-  constexpr int NS = gn_sums(OP), NC = gn_coefs(OP);
-  const int c0 = int(s / a.rows_cta), nc = int((e - 1) / a.rows_cta) - c0 + 1;
-  const int lanes = nc > 16 || a.wide ? 32 : nc > 8 ? 16 : 8;
-  const int sub = int(threadIdx.x) / lanes, lane = int(threadIdx.x) % lanes;
-  for (int base = 0; base < tl.nlg; base += GN_THREADS / lanes) {
-    const int lg = base + sub, g = tl.gfirst + (lg < tl.nlg ? lg : 0);
-    const RowBlock& blk = a.lay.blk[fast_div(uint32_t(g), a.lay.div_groups)];
-    const bool scalar = blk.bias0 >= 0;
-    int t0 = tl.t, nt = 1;
-    if (a.wide) {  // the tiles that hold parts of this group
-      while (t0 > 0 && group_of(a.lay, a.tile[t0] * VEC - 1) == g) --t0;
-      while (t0 + nt < a.n_tiles && group_of(a.lay, a.tile[t0 + nt] * VEC) == g) ++nt;
-    }
-    T S[NS];
-    gn_join<OP, T>(lg < tl.nlg ? nc * nt : 0, lane, lanes, 1, scalar, S, [&](int i) {
-      const int ch = c0 + (nt == 1 ? i : i / nt);
-      return gn_slot<OP, T>(a, ch, b, ch == c0, t0 + (nt == 1 ? 0 : i % nt), g);
-    });
-    if (lg < tl.nlg && lane == 0)
-      gn_finish<OP, T>(S, T(e - s) * T(blk.group_cols), scalar,
-                       a.stats + 2 * (int64_t(b) * a.lay.n_groups() + g), rc == c0, a.eps, res + NC * lg);
-  }
-}
-
-// Second pass over rows [lo, hi) of a tile.
-template <typename T, int VEC, int OP, bool DROP>
-__device__ __forceinline__ void gn_grid_second(const NormArgs& a, const GnTile& tl, int rc, int lo, int hi,
-                                               const GnGridSmem& sm) {
-  constexpr int NC = gn_coefs(OP);
-  const int tid = int(threadIdx.x), tx = tid % a.tx, ty = tid / a.tx;
-  const int64_t G = a.lay.n_groups();
-  const bool active = tx < tl.W && ty < a.k;
-  T* res = static_cast<T*>(sm.res);
-  GnCol<T, VEC, OP, DROP> c;
-  c.init(a, tl.v0, tl.W, active ? tx : 0);
-  double* colacc = nullptr;
-  if (OP == GN_DBL && a.colpart != nullptr) {
-    colacc = sm.columns + tid;
-#pragma unroll
-    for (int i = 0; i < 2 * VEC; ++i) colacc[i * GN_THREADS] = 0.0;
-  }
-#pragma unroll 1
-  for (int b = gn_first_segment(a, lo); b < a.B; ++b) {
-    int s, e;
-    gn_segment(a, b, s, e);
-    if (s >= hi) break;
-    const int ps = max(s, lo), pe = min(e, hi);
-    if (ps >= pe) continue;
-    const bool whole = ps == s && pe == e && !a.wide;
-    if (!whole) {
-      __syncthreads();
-      gn_grid_join<VEC, OP, T>(a, tl, rc, b, s, e, res);
-      __syncthreads();
-    }
-    if (!active) continue;
-    GnStat<T> st;
-    T kf[NC];
-    const T* q = whole ? static_cast<const T*>(a.coef) + NC * (b * G + c.g) : res + NC * c.lg;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) kf[i] = OP == GN_FWD && whole ? T(0) : q[i];
-    if (OP == GN_FWD && !whole) {
-      st.hi = kf[0];
-      st.lo = kf[1];
-      st.r = kf[2];
-    } else {
-      st.set(a.stats + 2 * (b * G + c.g));
-    }
-    if (c.kind == GN_PLAIN) gn_grid_apply<GN_PLAIN>(a, c, st, kf, ps, pe, ty, a.k, colacc);
-    else if (c.kind == GN_CENTRED) gn_grid_apply<GN_CENTRED>(a, c, st, kf, ps, pe, ty, a.k, colacc);
-    else gn_grid_apply<GN_ACT>(a, c, st, kf, ps, pe, ty, a.k, colacc);
-  }
-  if (active) gn_zero_rows<T, VEC, OP>(a, c.col, max(lo, gn_rows_end(a)) + ty, hi, a.k);
-  if (OP == GN_BWD && a.colpart != nullptr) gn_finish_columns<T, VEC>(a, a.chunks, tl.v0, tl.W, rc, a.chunks);
-  if (OP == GN_DBL && a.colpart != nullptr) gn_store_columns<VEC>(a, sm.columns, rc, tl.v0, tl.W, a.tx, a.k);
-}
-
-template <typename T, int VEC, int OP, bool DROP>
-__global__ void __launch_bounds__(GN_THREADS, OP == GN_FWD ? 3 : 2) gn_grid_kernel(const __grid_constant__ NormArgs a) {
-  using L = GnGrid<T, VEC, OP>;
-  extern __shared__ __align__(16) unsigned char smem[];
-  unsigned char* at = smem;
-  GnGridSmem sm;
-  sm.sums = reinterpret_cast<double*>(at);
-  sm.columns = reinterpret_cast<double*>(at += L::long_bytes);
-  sm.buf = at += L::col_bytes;
-  sm.res = at += L::buf_bytes;
-  sm.gs = reinterpret_cast<GnRange*>(at += L::res_bytes);
-  const int rc = int(blockIdx.x) / a.cx, ct = int(blockIdx.x) % a.cx;
-  const int lo = int(min(a.N, rc * a.rows_cta)), hi = int(min(a.N, (rc + 1) * a.rows_cta));
+  if (OP == GN_BWD && col_sums) gn_store_columns<VEC>(a, columns, rc, v0, W, a.tx, K);
   auto grid = cooperative_groups::this_grid();
-  const int slabs = (a.n_tiles + a.cx - 1) / a.cx;
-  // a CTA that has left its sums of slab s goes on with the second pass of slab s - 1 before it waits
+  grid.sync();
+
+  // join the segments that are spread over chunks (or tiles): chunk rc of nc takes groups rc - c0, + nc, ..
 #pragma unroll 1
-  for (int s = 0; s <= slabs; ++s) {
-    const int now = s * a.cx + ct, last = now - a.cx;
-    if (now < a.n_tiles) gn_grid_first<T, VEC, OP, DROP>(a, gn_tile<VEC>(a, now), rc, lo, hi, sm);
-    cooperative_groups::grid_group::arrival_token token{};
-    if (s < slabs) token = grid.barrier_arrive();
-    if (s > 0 && last < a.n_tiles) gn_grid_second<T, VEC, OP, DROP>(a, gn_tile<VEC>(a, last), rc, lo, hi, sm);
-    if (s < slabs) grid.barrier_wait(std::move(token));
+  for (p.b = first; p.next(a, lo, hi);) {
+    if (p.whole(a)) continue;
+    const int c0 = int(p.s / a.rows_cta), nc = int((p.e - 1) / a.rows_cta) - c0 + 1;
+    for (int lg = rc - c0 + nc * (tid / 32); lg < nlg; lg += nc * (GN_THREADS / 32)) {
+      const int g = gfirst + lg;
+      int nt = 1;
+      if (a.wide) {  // the tiles that hold parts of this group: the first one's CTA joins it
+        if (tile > 0 && group_of(a.lay, v0 * VEC - 1) == g) continue;
+        while (tile + nt < a.n_tiles && group_of(a.lay, a.tile[tile + nt] * VEC) == g) ++nt;
+      }
+      const RowBlock& blk = a.lay.blk[fast_div(uint32_t(g), a.lay.div_groups)];
+      const bool scalar = blk.bias0 >= 0;
+      T S[NS];
+      gn_join<OP, T, 8>(nc * nt, tid % 32, 32, 1, scalar, S, [&](int i) {
+        const int ch = c0 + (nt == 1 ? i : i / nt);
+        return gn_slot<OP, T>(a, ch, p.b, ch == c0, tile + (nt == 1 ? 0 : i % nt), g);
+      });
+      if (tid % 32 == 0) {
+        T o[NC];
+        const T r = OP == GN_DBL ? T(a.stats[2 * (p.b * G + g) + 1]) : T(0);
+        gn_finish<OP, T>(S, T(p.e - p.s) * T(blk.group_cols), scalar, r, T(a.eps), o);
+        keep(o, p.b, g);
+      }
+    }
   }
-  if (OP == GN_DBL && a.colpart != nullptr) {
+  p.b = first;
+  there = open(true);  // the second pass' first rows are on their way while the grid meets
+  if (OP == GN_BWD && col_sums) gn_finish_columns<T, VEC>(a, a.chunks, v0, W, rc, a.chunks);
+  grid.sync();
+
+  // second pass
+#pragma unroll 1
+  for (; there; there = open(true)) {
+    GnStat<T> st;
+    st.set(a.stats + 2 * (p.b * G + c.g));
+    T kf[NC];
+    if (OP != GN_FWD) {
+      const T* k = static_cast<const T*>(a.coef) + NC * (p.b * G + c.g);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) kf[i] = k[i];
+    }
+    double* acc = OP == GN_DBL ? colacc : nullptr;
+    if (c.kind == GN_PLAIN) gn_grid_apply<GN_PLAIN>(a, c, st, kf, q, p.ps + ty, n, K, acc);
+    else if (c.kind == GN_CENTRED) gn_grid_apply<GN_CENTRED>(a, c, st, kf, q, p.ps + ty, n, K, acc);
+    else gn_grid_apply<GN_ACT>(a, c, st, kf, q, p.ps + ty, n, K, acc);
+  }
+  if (active) gn_zero_rows<T, VEC, OP>(a, c.col, max(lo, gn_rows_end(a)) + ty, hi, K);
+  if (OP == GN_DBL && col_sums) {
+    gn_store_columns<VEC>(a, columns, rc, v0, W, a.tx, K);
     grid.sync();
-    for (int t = ct; t < a.n_tiles; t += a.cx)
-      gn_finish_columns<T, VEC>(a, a.chunks, a.tile[t], a.tile[t + 1] - a.tile[t], rc, a.chunks);
+    gn_finish_columns<T, VEC>(a, a.chunks, v0, W, rc, a.chunks);
   }
 }
 

@@ -9,16 +9,19 @@ namespace e3b {
 
 static_assert(sizeof(NormArgs) <= 4096, "kernel arguments");
 
+// Threads of a CTA of the local kernel when every segment is one row: rows are wide, batches short.
+constexpr int GN_ROW_THREADS = 512;
+
 struct GnConfig {
   bool local = false;
   bool one_row = false;   // local: no segment has more than one row
   int64_t max_ctas = 0;   // local: CTAs along the segments that have work
   size_t ws_bytes = 0;
 };
-// rows that a thread of the local kernel keeps in registers; segments that share them when every
+// rows that a thread of the local kernel holds; segments that share them when every
 // segment is one row
-__host__ __device__ constexpr int gn_reg_rows(int op) { return op == GN_DBL ? 4 : 8; }
-__host__ __device__ constexpr int gn_reg_segments(int op) { return op == GN_FWD ? 8 : op == GN_BWD ? 4 : 2; }
+__host__ __device__ constexpr int gn_reg_rows(int op) { return op == GN_FWD ? 8 : op == GN_BWD ? 4 : 2; }
+__host__ __device__ constexpr int gn_reg_segments(int op) { return op == GN_FWD ? 4 : op == GN_BWD ? 2 : 1; }
 
 // Chunks and workspace of the grid kernel on `ctas` resident CTAs; returns the bytes needed.
 size_t gn_grid_layout(NormArgs* a, int op, int elem, int64_t ctas);
@@ -32,29 +35,32 @@ e3_status gn_launch_dbl(NormArgs& a, const GnConfig& c, bool f64, int vec, bool 
 
 // CTAs of `kernel` that are resident together on the current device (found once per device).
 template <typename K>
-int gn_resident(K kernel, size_t smem, std::atomic<int>* cache, bool cluster) {
+int gn_resident(K kernel, size_t smem, std::atomic<int64_t>* cache, bool cluster, int threads = GN_THREADS) {
   int dev = 0;
   cudaGetDevice(&dev);
-  int n = dev < 64 ? cache[dev].load(std::memory_order_relaxed) : 0;
+  // the cache holds the answer for the last size asked for (sizes differ by a few hundred bytes at most)
+  const int64_t hit = dev < 64 ? cache[dev].load(std::memory_order_relaxed) : 0;
+  int n = hit >> 32 == int64_t(smem) ? int(hit & 0xFFFFFFFF) : 0;
   if (n == 0) {
     int per = 0;
     if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
       return 0;
     if (cluster && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
       return 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, GN_THREADS, smem) != cudaSuccess) return 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem) != cudaSuccess) return 0;
     n = std::min(per, GN_MAX_RESIDENT) * sm_count();
-    if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+    if (dev < 64) cache[dev].store(int64_t(smem) << 32 | n, std::memory_order_relaxed);
   }
   return n;
 }
 
 template <typename K>
-e3_status gn_start(K kernel, const NormArgs& a, dim3 grid, size_t smem, bool meet, int cluster, cudaStream_t s) {
+e3_status gn_start(K kernel, const NormArgs& a, dim3 grid, size_t smem, bool meet, int cluster, cudaStream_t s,
+                   int threads = GN_THREADS) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(GN_THREADS);
+  cfg.blockDim = dim3(unsigned(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -76,12 +82,12 @@ e3_status gn_start(K kernel, const NormArgs& a, dim3 grid, size_t smem, bool mee
   return E3_OK;
 }
 
-template <typename T, int VEC, int OP, bool DROP, int R, int M, bool CL>
+template <typename T, int VEC, int OP, bool DROP, int R, int M, bool CL, int NT = GN_THREADS>
 e3_status gn_run_local(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s) {
-  static std::atomic<int> cache[64];
-  constexpr size_t smem = GnLocal<T, VEC, OP, R, M, CL>::smem;
-  auto kernel = gn_local_kernel<T, VEC, OP, DROP, R, M, CL>;
-  const int q = gn_resident(kernel, smem, cache, CL);
+  static std::atomic<int64_t> cache[64];
+  const size_t smem = GnLocal<T, VEC, OP, R, M, CL, NT>::smem(a);
+  auto kernel = gn_local_kernel<T, VEC, OP, DROP, R, M, CL, NT>;
+  const int q = gn_resident(kernel, smem, cache, CL, NT);
   int64_t room = q / a.n_tiles / a.cs;  // clusters along the segments that are resident together
   if (CL) {
     static std::atomic<int> clusters[64][5];
@@ -112,21 +118,21 @@ e3_status gn_run_local(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s)
   if (gn_local_layout(&a, OP, parts) > c.ws_bytes) return fail(E3_ERR_SHAPE, "group norm: workspace too small");
   const bool columns = OP != GN_FWD && (a.gw != nullptr || a.gb != nullptr);
   a.colpart = columns ? static_cast<double*>(ws) : nullptr;
-  return gn_start(kernel, a, dim3(unsigned(parts), unsigned(a.n_tiles)), smem, columns, a.cs, s);
+  return gn_start(kernel, a, dim3(unsigned(parts), unsigned(a.n_tiles)), smem, columns, a.cs, s, NT);
 }
 
 template <typename T, int VEC, int OP, bool DROP>
 e3_status gn_run(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s) {
   if (c.local) {
-    if (c.one_row) return gn_run_local<T, VEC, OP, DROP, 1, gn_reg_segments(OP), false>(a, c, ws, s);
+    if (c.one_row) return gn_run_local<T, VEC, OP, DROP, 1, gn_reg_segments(OP), false, GN_ROW_THREADS>(a, c, ws, s);
     if (a.cs > 1) return gn_run_local<T, VEC, OP, DROP, gn_reg_rows(OP), 1, true>(a, c, ws, s);
     return gn_run_local<T, VEC, OP, DROP, gn_reg_rows(OP), 1, false>(a, c, ws, s);
   }
-  static std::atomic<int> cache[64];
+  static std::atomic<int64_t> cache[64];
   constexpr size_t smem = GnGrid<T, VEC, OP>::smem;
   auto kernel = gn_grid_kernel<T, VEC, OP, DROP>;
   const int q = gn_resident(kernel, smem, cache, false);
-  if (q == 0) return fail(E3_ERR_CUDA, "group norm: no room for the kernel on this device");
+  if (q < a.n_tiles) return fail(E3_ERR_CUDA, "group norm: no room for the kernel on this device");
   if (gn_grid_layout(&a, OP, int(sizeof(T)), q) > c.ws_bytes)
     return fail(E3_ERR_SHAPE, "group norm: workspace too small");
   char* base = static_cast<char*>(ws);
@@ -134,7 +140,7 @@ e3_status gn_run(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s) {
   a.coef = base + reinterpret_cast<size_t>(a.coef);
   const bool columns = OP != GN_FWD && (a.gw != nullptr || a.gb != nullptr);
   a.colpart = columns ? reinterpret_cast<double*>(base + reinterpret_cast<size_t>(a.colpart)) : nullptr;
-  return gn_start(kernel, a, dim3(unsigned(a.chunks) * unsigned(a.cx)), smem, true, 1, s);
+  return gn_start(kernel, a, dim3(unsigned(a.chunks) * unsigned(a.n_tiles)), smem, true, 1, s);
 }
 
 template <int OP>

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 
 #include "features.h"
 
@@ -30,6 +31,29 @@ __host__ __device__ __forceinline__ uint32_t fast_div(uint32_t x, uint32_t recip
 #else
   return recip ? uint32_t((uint64_t(x) * recip) >> 32) : x;
 #endif
+}
+
+// The same for rows that are not needed again: they leave L2 first.
+template <typename T, int VEC>
+__device__ __forceinline__ RowVec<T, VEC> load_row_last(const T* p) {
+  RowVec<T, VEC> r;
+  if constexpr (sizeof(T) * VEC == 16) {
+    const int4 q = __ldcs(reinterpret_cast<const int4*>(p));
+    memcpy(&r, &q, 16);
+  } else {
+    r.v[0] = __ldcs(p);
+  }
+  return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_row_last(T* p, const RowVec<T, VEC>& v) {
+  if constexpr (sizeof(T) * VEC == 16) {
+    int4 q;
+    memcpy(&q, &v, 16);
+    __stcs(reinterpret_cast<int4*>(p), q);
+  } else {
+    __stcs(p, v.v[0]);
+  }
 }
 
 // Block of a column.
