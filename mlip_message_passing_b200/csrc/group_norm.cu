@@ -215,6 +215,9 @@ void make_tiles(e3_features* f) {
   f->cluster_ok = f->narrow.n() > 0 && f->narrow.n() <= 64 && f->narrow.groups <= 32;
 }
 
+// Bytes that a CTA reads per part of the second pass.
+constexpr int64_t GN_PART_BYTES = 64 << 10;
+
 size_t gn_grid_layout(NormArgs* a, int op, int elem, int64_t ctas) {
   (void)elem;
   const int64_t most = std::max<int64_t>(1, ctas / a->n_tiles);
@@ -224,10 +227,15 @@ size_t gn_grid_layout(NormArgs* a, int op, int elem, int64_t ctas) {
   const size_t slots = a->wide ? size_t(most) + size_t(a->B) : 2 * size_t(most);
   const size_t coef = al256(slots * (G + size_t(a->n_tiles)) * gn_sums(op) * 8);
   const size_t col = coef + (op == GN_FWD ? 0 : al256(size_t(a->B) * G * gn_coefs(op) * 8));
+  // about 64 KB of a chunk's first array at a time
+  const int64_t bytes = a->rows_cta * a->tx * (op == GN_FWD ? 16 : 32);
+  a->parts = op == GN_DBL ? 1 : int32_t(std::min<int64_t>(16, std::max<int64_t>(1, bytes / GN_PART_BYTES)));
+  const size_t tickets = col + (op == GN_FWD ? 0 : al256(size_t(most) * 2 * size_t(a->lay.dim) * 8));
   a->part = nullptr;
   a->coef = reinterpret_cast<void*>(coef);   // offsets; the launcher adds the base
   a->colpart = reinterpret_cast<double*>(col);
-  return std::max<size_t>(256, col + (op == GN_FWD ? 0 : al256(size_t(most) * 2 * size_t(a->lay.dim) * 8)));
+  a->tickets = reinterpret_cast<int32_t*>(tickets);
+  return tickets + al256(size_t(a->n_tiles) * 4);
 }
 
 size_t gn_local_layout(NormArgs* a, int op, int64_t parts) {

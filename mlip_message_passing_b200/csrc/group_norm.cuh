@@ -70,6 +70,8 @@ struct NormArgs {
   int32_t tile_groups;      // most groups that a tile holds (parts of)
   int32_t chunks;           // grid: row chunks
   int64_t rows_cta;         // grid: rows of a chunk
+  int32_t parts;            // grid: parts of a chunk in the second pass
+  int32_t* tickets;         // grid: next part of each tile
   DropArgs drop;
   RowLayout lay;
   int32_t tile[GN_MAXTILE + 1];  // first vector column of each tile
@@ -1089,7 +1091,7 @@ __global__ void __launch_bounds__(GN_THREADS, OP == GN_FWD ? 3 : 2) gn_grid_kern
   T* buf = reinterpret_cast<T*>(smem + L::slot_bytes + L::long_bytes + L::col_bytes);
   GnRange* gs = reinterpret_cast<GnRange*>(smem + L::slot_bytes + L::long_bytes + L::col_bytes + L::buf_bytes);
   const int rc = int(blockIdx.x) / a.n_tiles, tile = int(blockIdx.x) % a.n_tiles;
-  const int lo = int(min(a.N, rc * a.rows_cta)), hi = int(min(a.N, (rc + 1) * a.rows_cta));
+  int lo = int(min(a.N, rc * a.rows_cta)), hi = int(min(a.N, (rc + 1) * a.rows_cta));
   const int tid = int(threadIdx.x), tx = tid % a.tx, ty = tid / a.tx, K = a.k;
   const int v0 = a.tile[tile], W = a.tile[tile + 1] - v0;
   const bool active = tx < W && ty < K;
@@ -1097,7 +1099,7 @@ __global__ void __launch_bounds__(GN_THREADS, OP == GN_FWD ? 3 : 2) gn_grid_kern
 
   GnStream<T, VEC, OP> q;
   q.sl.init(a, smem);
-  const int first = gn_first_segment(a, lo) - 1;
+  int first = gn_first_segment(a, lo) - 1;
   GnPiece p;
   int n = 0;  // this thread's rows of the piece
   auto open = [&](bool back) {
@@ -1169,6 +1171,7 @@ __global__ void __launch_bounds__(GN_THREADS, OP == GN_FWD ? 3 : 2) gn_grid_kern
     __syncthreads();
   }
   if (OP == GN_BWD && col_sums) gn_store_columns<VEC>(a, columns, rc, v0, W, a.tx, K);
+  if (rc == 0 && tid == 0) a.tickets[tile] = a.chunks;  // the first parts are handed out already
   auto grid = cooperative_groups::this_grid();
   grid.sync();
 
@@ -1177,7 +1180,8 @@ __global__ void __launch_bounds__(GN_THREADS, OP == GN_FWD ? 3 : 2) gn_grid_kern
   for (p.b = first; p.next(a, lo, hi);) {
     if (p.whole(a)) continue;
     const int c0 = int(p.s / a.rows_cta), nc = int((p.e - 1) / a.rows_cta) - c0 + 1;
-    for (int lg = rc - c0 + nc * (tid / 32); lg < nlg; lg += nc * (GN_THREADS / 32)) {
+#pragma unroll 1
+    for (int lg = rc - c0; lg < nlg; lg += nc) {
       const int g = gfirst + lg;
       int nt = 1;
       if (a.wide) {  // the tiles that hold parts of this group: the first one's CTA joins it
@@ -1186,41 +1190,80 @@ __global__ void __launch_bounds__(GN_THREADS, OP == GN_FWD ? 3 : 2) gn_grid_kern
       }
       const RowBlock& blk = a.lay.blk[fast_div(uint32_t(g), a.lay.div_groups)];
       const bool scalar = blk.bias0 >= 0;
+      // every warp its share of the entries, then one warp the warps' sums
+      constexpr int WARPS = GN_THREADS / 32;
+      const int w = tid / 32, E = nc * nt, mine = E > w ? (E - w + WARPS - 1) / WARPS : 0;
+      const T* part = gn_slot<OP, T>(a, c0, p.b, false, tile, g);
+      const int64_t hop = (a.wide ? 1 : 2) * (G + a.n_tiles) * NS;  // from chunk to chunk
+      const int64_t begin = a.wide ? 0 : (G + a.n_tiles) * NS;      // the first chunk's slot is the next one
       T S[NS];
-      gn_join<OP, T, 8>(nc * nt, tid % 32, 32, 1, scalar, S, [&](int i) {
-        const int ch = c0 + (nt == 1 ? i : i / nt);
-        return gn_slot<OP, T>(a, ch, p.b, ch == c0, tile + (nt == 1 ? 0 : i % nt), g);
+      gn_join<OP, T, 2>(mine, tid % 32, 32, 1, scalar, S, [&](int i) {
+        const int e = w + i * WARPS, ch = nt == 1 ? e : e / nt;
+        return part + ch * hop + (ch == 0 ? begin : 0) + (nt == 1 ? 0 : (e - ch * nt) * NS);
       });
       if (tid % 32 == 0) {
-        T o[NC];
-        const T r = OP == GN_DBL ? T(a.stats[2 * (p.b * G + g) + 1]) : T(0);
-        gn_finish<OP, T>(S, T(p.e - p.s) * T(blk.group_cols), scalar, r, T(a.eps), o);
-        keep(o, p.b, g);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) buf[w * NS + i] = S[i];
       }
+      __syncthreads();
+      if (w == 0) {
+        gn_join<OP, T>(min(WARPS, E), tid, 32, 1, scalar, S, [&](int i) { return buf + i * NS; });
+        if (tid == 0) {
+          T o[NC];
+          const T r = OP == GN_DBL ? T(a.stats[2 * (p.b * G + g) + 1]) : T(0);
+          gn_finish<OP, T>(S, T(p.e - p.s) * T(blk.group_cols), scalar, r, T(a.eps), o);
+          keep(o, p.b, g);
+        }
+      }
+      __syncthreads();
     }
   }
+  // second pass: the chunks are cut into parts, the last ones first.  Without sums to keep (all forms but
+  // the double backward) a CTA that is done draws another part of its tile: the CTAs' shares of the memory
+  // bandwidth differ by a third, and the slowest would hold up the rest.
+  int part = rc;
+  auto bounds = [&]() {  // rows of part `part` of the tile
+    if (a.parts == 1) return;
+    const int ch = part % a.chunks, at = a.parts - 1 - part / a.chunks;
+    const int64_t c_lo = ch * a.rows_cta, c_hi = min(a.N, c_lo + a.rows_cta);
+    const int64_t size = (a.rows_cta + a.parts - 1) / a.parts;
+    lo = int(min(c_hi, c_lo + at * size));
+    hi = int(min(c_hi, c_lo + (at + 1) * size));
+    first = gn_first_segment(a, lo) - 1;
+  };
+  bounds();
   p.b = first;
-  there = open(true);  // the second pass' first rows are on their way while the grid meets
+  there = lo < hi && open(true);  // the first rows are on their way while the grid meets
   if (OP == GN_BWD && col_sums) gn_finish_columns<T, VEC>(a, a.chunks, v0, W, rc, a.chunks);
   grid.sync();
 
-  // second pass
+  while (true) {
+    if (a.parts > 1 && tid == 0) gs[0].first = atomicAdd(a.tickets + tile, 1);
 #pragma unroll 1
-  for (; there; there = open(true)) {
-    GnStat<T> st;
-    st.set(a.stats + 2 * (p.b * G + c.g));
-    T kf[NC];
-    if (OP != GN_FWD) {
-      const T* k = static_cast<const T*>(a.coef) + NC * (p.b * G + c.g);
+    for (; there; there = open(true)) {
+      GnStat<T> st;
+      st.set(a.stats + 2 * (p.b * G + c.g));
+      T kf[NC];
+      if (OP != GN_FWD) {
+        const T* k = static_cast<const T*>(a.coef) + NC * (p.b * G + c.g);
 #pragma unroll
-      for (int i = 0; i < NC; ++i) kf[i] = k[i];
+        for (int i = 0; i < NC; ++i) kf[i] = k[i];
+      }
+      double* acc = OP == GN_DBL ? colacc : nullptr;
+      if (c.kind == GN_PLAIN) gn_grid_apply<GN_PLAIN>(a, c, st, kf, q, p.ps + ty, n, K, acc);
+      else if (c.kind == GN_CENTRED) gn_grid_apply<GN_CENTRED>(a, c, st, kf, q, p.ps + ty, n, K, acc);
+      else gn_grid_apply<GN_ACT>(a, c, st, kf, q, p.ps + ty, n, K, acc);
     }
-    double* acc = OP == GN_DBL ? colacc : nullptr;
-    if (c.kind == GN_PLAIN) gn_grid_apply<GN_PLAIN>(a, c, st, kf, q, p.ps + ty, n, K, acc);
-    else if (c.kind == GN_CENTRED) gn_grid_apply<GN_CENTRED>(a, c, st, kf, q, p.ps + ty, n, K, acc);
-    else gn_grid_apply<GN_ACT>(a, c, st, kf, q, p.ps + ty, n, K, acc);
+    if (active) gn_zero_rows<T, VEC, OP>(a, c.col, max(lo, gn_rows_end(a)) + ty, hi, K);
+    if (a.parts == 1) break;
+    __syncthreads();
+    part = gs[0].first;
+    __syncthreads();
+    if (part >= a.chunks * a.parts) break;
+    bounds();
+    p.b = first;
+    there = lo < hi && open(true);
   }
-  if (active) gn_zero_rows<T, VEC, OP>(a, c.col, max(lo, gn_rows_end(a)) + ty, hi, K);
   if (OP == GN_DBL && col_sums) {
     gn_store_columns<VEC>(a, columns, rc, v0, W, a.tx, K);
     grid.sync();

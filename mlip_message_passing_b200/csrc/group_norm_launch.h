@@ -137,6 +137,7 @@ e3_status gn_run(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s) {
     return fail(E3_ERR_SHAPE, "group norm: workspace too small");
   char* base = static_cast<char*>(ws);
   a.part = base;
+  a.tickets = reinterpret_cast<int32_t*>(base + reinterpret_cast<size_t>(a.tickets));
   a.coef = base + reinterpret_cast<size_t>(a.coef);
   const bool columns = OP != GN_FWD && (a.gw != nullptr || a.gb != nullptr);
   a.colpart = columns ? reinterpret_cast<double*>(base + reinterpret_cast<size_t>(a.colpart)) : nullptr;
