@@ -387,8 +387,8 @@ typedef enum { E3_ACT_NONE = 0, E3_ACT_SILU = 1 } e3_act;
  *   drop     NULL: none;
  *   stats    device [B, n_groups, 2] doubles: (mu, r), written by the forward (unspecified for an empty
  *            segment), read by the backward;
- *   workspace  device buffer of e3_group_norm_workspace_size bytes, 16-byte aligned, not used by any
- *            other call while this one runs on its stream.
+ *   workspace  device buffer of e3_group_norm_workspace_size bytes (it covers all three calls; 0: may
+ *            be NULL), 16-byte aligned, not used by any other call while this one runs on its stream.
  * Sums run in the rows' type over at most 64 rows of a thread, and over a segment that fits one block
  * of threads; in double from there on.  Their order is fixed: results are bitwise repeatable.  N < 2^31, 1 <= B < 2^31.  N == 0 leaves every row output alone and
  * zero-fills the parameters' gradients. */

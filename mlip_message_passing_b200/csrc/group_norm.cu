@@ -107,10 +107,11 @@ GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows,
     const int k = GN_THREADS / n->tx;
     int cs = 1;
     while (cs < 16 && int64_t(RP) * k * cs < most) cs *= 2;
-    // the backwards' clusters meet for the parameters' gradients: one per tile has to be resident
-    const bool fits = int64_t(RP) * k * cs >= most && (op == GN_FWD || n->n() * cs <= 128);
+    // all clusters at once (in the backwards they meet for the parameters' gradients, on one CTA per SM)
+    const int64_t all = B * n->n();
+    const bool fits = int64_t(RP) * k * cs >= most && all * cs <= (op == GN_FWD ? 2 * sm_count() : 128);
     if (fits && (!c.local || (a->j == 1 && int64_t(t->n()) * B < sm_count()))) {
-      while (cs < 8 && int64_t(n->n()) * B * cs * 2 <= (op == GN_FWD ? 2 * sm_count() : 128) && most > 2 * k * cs) cs *= 2;
+      while (cs < 8 && all * cs * 2 <= (op == GN_FWD ? 2 * sm_count() : 128) && most > 2 * k * cs) cs *= 2;
       c.local = true;
       t = n;
       a->k = k;
@@ -135,16 +136,17 @@ GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows,
 }
 
 e3_status check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (need == 0) return E3_OK;
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 15u))
     return fail(E3_ERR_INVALID_ARG, "workspace is NULL or not 16-byte aligned");
   if (bytes < need) return fail(E3_ERR_SHAPE, "workspace of %zu bytes, %zu needed", bytes, need);
   return E3_OK;
 }
 
-size_t workspace_bytes_of(const GnConfig& c, NormArgs a, e3_dtype dtype, int op) {
+size_t workspace_bytes_of(const GnConfig& c, NormArgs a, int op) {
   const int64_t ctas = int64_t(GN_MAX_RESIDENT) * sm_count();
-  if (c.local) return std::max<size_t>(256, gn_local_layout(&a, op, std::max<int64_t>(1, ctas / a.n_tiles)));
-  return gn_grid_layout(&a, op, dtype == E3_F64 ? 8 : 4, ctas);
+  if (c.local) return gn_local_layout(&a, op, std::max<int64_t>(1, ctas / a.n_tiles));
+  return gn_grid_layout(&a, op, ctas);
 }
 
 e3_status check_sizes(const e3_features* f, int64_t N, int64_t B, bool one_ok) {
@@ -179,7 +181,7 @@ e3_status begin(const e3_features* f, int64_t N, int64_t B, const int32_t* row_p
   if ((st = drop_args(drop, N, &a->drop, drop_on)) != E3_OK) return st;
   *c = configure(f, N, B, max_rows, op, a);
   c->ws_bytes = ws_bytes;
-  if (N > 0 && (st = check_workspace(ws, ws_bytes, workspace_bytes_of(*c, *a, f->dtype, op))) != E3_OK) return st;
+  if (N > 0 && (st = check_workspace(ws, ws_bytes, workspace_bytes_of(*c, *a, op))) != E3_OK) return st;
   if ((st = ensure_device_tables()) != E3_OK) return st;
   if ((st = device_status_ptr(&a->status)) != E3_OK) return st;
   a->row_ptr = row_ptr;
@@ -215,11 +217,11 @@ void make_tiles(e3_features* f) {
   f->cluster_ok = f->narrow.n() > 0 && f->narrow.n() <= 64 && f->narrow.groups <= 32;
 }
 
-// Bytes that a CTA reads per part of the second pass.
-constexpr int64_t GN_PART_BYTES = 64 << 10;
+// Bytes that a CTA reads for one part of the second pass (64 to 512 KB: 110 to 107 us for the forward of
+// 24000 x 2048 floats, 203 to 191 us for the backward; parts start with an empty pipeline).
+constexpr int64_t GN_PART_BYTES = 512 << 10;
 
-size_t gn_grid_layout(NormArgs* a, int op, int elem, int64_t ctas) {
-  (void)elem;
+size_t gn_grid_layout(NormArgs* a, int op, int64_t ctas) {
   const int64_t most = std::max<int64_t>(1, ctas / a->n_tiles);
   a->rows_cta = std::max<int64_t>((a->N + most - 1) / most, 2 * a->k);
   a->chunks = int32_t(std::max<int64_t>(1, (a->N + a->rows_cta - 1) / a->rows_cta));
@@ -227,7 +229,6 @@ size_t gn_grid_layout(NormArgs* a, int op, int elem, int64_t ctas) {
   const size_t slots = a->wide ? size_t(most) + size_t(a->B) : 2 * size_t(most);
   const size_t coef = al256(slots * (G + size_t(a->n_tiles)) * gn_sums(op) * 8);
   const size_t col = coef + (op == GN_FWD ? 0 : al256(size_t(a->B) * G * gn_coefs(op) * 8));
-  // about 64 KB of a chunk's first array at a time
   const int64_t bytes = a->rows_cta * a->tx * (op == GN_FWD ? 16 : 32);
   a->parts = op == GN_DBL ? 1 : int32_t(std::min<int64_t>(16, std::max<int64_t>(1, bytes / GN_PART_BYTES)));
   const size_t tickets = col + (op == GN_FWD ? 0 : al256(size_t(most) * 2 * size_t(a->lay.dim) * 8));
@@ -256,7 +257,7 @@ extern "C" e3_status e3_group_norm_workspace_size(const e3_features* f, int64_t 
   for (int op = GN_FWD; op <= GN_DBL; ++op) {
     NormArgs a{};
     const GnConfig c = configure(f, N, B, max_rows, op, &a);
-    *bytes = std::max(*bytes, workspace_bytes_of(c, a, f->dtype, op));
+    *bytes = std::max(*bytes, workspace_bytes_of(c, a, op));
   }
   return E3_OK;
 }

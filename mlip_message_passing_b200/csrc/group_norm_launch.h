@@ -24,7 +24,7 @@ __host__ __device__ constexpr int gn_reg_rows(int op) { return op == GN_FWD ? 8 
 __host__ __device__ constexpr int gn_reg_segments(int op) { return op == GN_FWD ? 4 : op == GN_BWD ? 2 : 1; }
 
 // Chunks and workspace of the grid kernel on `ctas` resident CTAs; returns the bytes needed.
-size_t gn_grid_layout(NormArgs* a, int op, int elem, int64_t ctas);
+size_t gn_grid_layout(NormArgs* a, int op, int64_t ctas);
 size_t gn_local_layout(NormArgs* a, int op, int64_t parts);
 // Most CTAs that any kernel here keeps resident on an SM (sizes workspaces).
 constexpr int GN_MAX_RESIDENT = 8;
@@ -133,7 +133,7 @@ e3_status gn_run(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s) {
   auto kernel = gn_grid_kernel<T, VEC, OP, DROP>;
   const int q = gn_resident(kernel, smem, cache, false);
   if (q < a.n_tiles) return fail(E3_ERR_CUDA, "group norm: no room for the kernel on this device");
-  if (gn_grid_layout(&a, OP, int(sizeof(T)), q) > c.ws_bytes)
+  if (gn_grid_layout(&a, OP, q) > c.ws_bytes)
     return fail(E3_ERR_SHAPE, "group norm: workspace too small");
   char* base = static_cast<char*>(ws);
   a.part = base;

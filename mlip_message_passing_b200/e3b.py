@@ -680,7 +680,9 @@ class Features:
         vals = [ctypes.c_int64() for _ in range(4)]
         _check(lib.e3_features_info(handle, *(ctypes.byref(v) for v in vals)))
         self.dim, self.n_channels, self.n_scalars, self.n_groups = (v.value for v in vals)
-        self.device = torch.device("cuda", torch.cuda.current_device()) if torch.cuda.is_available() else None
+        self.index = torch.cuda.current_device() if torch.cuda.is_available() else None
+        self.device = None if self.index is None else torch.device("cuda", self.index)
+        self.workspace_bytes = {}  # sizes by (rows, segments, max_rows)
 
     def __del__(self):
         if getattr(self, "_handle", None) and lib is not None:
@@ -732,23 +734,41 @@ class Segments:
         return cls(ptr.to(device), n_rows, max_rows=max(counts))
 
 
+def _rows(t, name, features, shape):
+    """`_need` for the operands of the row operators, with the common case first: these calls take a few
+    microseconds on small inputs."""
+    if not (type(t) is torch.Tensor and t.dtype is features.dtype and t.shape == shape and t.is_contiguous()
+            and t.is_cuda and t.get_device() == features.index):
+        _need(t, name, features.dtype, shape, features.device)
+    return t.data_ptr()
+
+
+def _opt_rows(t, name, features, shape):
+    return None if t is None else _rows(t, name, features, shape)
+
+
+def _row_stream(features):
+    """The current stream's handle; the features' device has to be current (the library checks it)."""
+    return torch._C._cuda_getCurrentRawStream(features.index)
+
+
 def _drop_spec(features, p, rng, row0):
-    """The C dropout argument, or None when nothing is dropped."""
+    """The C dropout argument (by reference), or None when nothing is dropped."""
+    if p == 0:
+        return None
     p = float(p)
     if not 0.0 <= p < 1.0:
         raise ValueError(f"p must be in [0, 1), got {p}")
-    if p == 0.0:
-        return None
     if rng is None:
         raise ValueError("dropout needs rng: a seed, a (seed, offset) pair or an int64 CUDA tensor [2]")
     if isinstance(rng, torch.Tensor):
         _need(rng, "rng", torch.int64, (2,), features.device)
-        return DropoutSpec(p, 0, 0, rng.data_ptr(), int(row0))
+        return ctypes.byref(DropoutSpec(p, 0, 0, rng.data_ptr(), int(row0)))
     seed, offset = rng if isinstance(rng, (tuple, list)) else (rng, 0)
     seed, offset = int(seed), int(offset)
     if not -2 ** 63 <= seed < 2 ** 64 or not 0 <= offset < 2 ** 32:
         raise ValueError("the seed must fit 64 bits, the offset 32")
-    return DropoutSpec(p, seed % 2 ** 64, offset, None, int(row0))
+    return ctypes.byref(DropoutSpec(p, seed % 2 ** 64, offset, None, int(row0)))
 
 
 def dropout_forward(features, x, p, rng, residual=None, row0=0, out=None):
@@ -757,18 +777,14 @@ def dropout_forward(features, x, p, rng, residual=None, row0=0, out=None):
     runs (for captured programs).  ``row0``: index of the first row in a larger, sharded array.
     ``out`` may be x or residual.  The mask depends on rng, row and channel only, so the gradient
     with respect to x is this call on the gradient."""
-    N, dt, dev = x.shape[0], features.dtype, features.device
+    N = x.shape[0]
     shape = (N, features.dim)
-    _need(x, "x", dt, shape, dev)
-    if residual is not None:
-        _need(residual, "residual", dt, shape, dev)
+    px = _rows(x, "x", features, shape)
+    pr = _opt_rows(residual, "residual", features, shape)
     if out is None:
         out = torch.empty_like(x)
-    else:
-        _need(out, "out", dt, shape, dev)
-    spec = _drop_spec(features, p, rng, row0)
-    _check(lib.e3_dropout(features.handle, N, _ptr(x), _ptr(residual), None if spec is None else ctypes.byref(spec),
-                          _ptr(out), _stream()))
+    _check(lib.e3_dropout(features.handle, N, px, pr, _drop_spec(features, p, rng, row0),
+                          _rows(out, "out", features, shape), _row_stream(features)))
     return out
 
 
@@ -796,27 +812,35 @@ def dropout(features, x, p, rng, residual=None, row0=0):
 
 
 def _norm_args(features, x, weight, bias, segments, act):
-    N, dt, dev = x.shape[0], features.dtype, features.device
-    _need(x, "x", dt, (N, features.dim), dev)
-    if weight is not None:
-        _need(weight, "weight", dt, (features.n_channels,), dev)
-    if bias is not None:
-        _need(bias, "bias", dt, (features.n_scalars,), dev)
+    """(N, B, row_ptr, max_rows, x, weight, bias) as the C calls take them."""
+    N = x.shape[0]
+    px = _rows(x, "x", features, (N, features.dim))
+    pw = _opt_rows(weight, "weight", features, (features.n_channels,))
+    pb = _opt_rows(bias, "bias", features, (features.n_scalars,))
     if act not in _ACTS:
         raise ValueError(f"act must be None or 'silu', got {act!r}")
     if segments is None:
-        return N, 1, None, N
+        return N, 1, None, N, px, pw, pb
     if segments.n_rows != N:
         raise ValueError(f"x has {N} rows, the segments were made for {segments.n_rows}")
-    if segments.row_ptr.device != dev:
-        raise ValueError(f"segments are on {segments.row_ptr.device}, expected {dev}")
-    return N, segments.n_segments, segments.row_ptr, segments.max_rows
+    if segments.row_ptr.get_device() != features.index:
+        raise ValueError(f"segments are on {segments.row_ptr.device}, expected {features.device}")
+    return N, segments.n_segments, segments.row_ptr.data_ptr(), segments.max_rows, px, pw, pb
 
 
 def _norm_workspace(features, N, B, max_rows):
-    nbytes = ctypes.c_size_t()
-    _check(lib.e3_group_norm_workspace_size(features.handle, N, B, max_rows, ctypes.byref(nbytes)))
-    return torch.empty(nbytes.value, dtype=torch.uint8, device=features.device)
+    """(tensor or None, pointer, bytes); a new buffer each time, so that calls in flight never share one."""
+    n = features.workspace_bytes.get((N, B, max_rows))
+    if n is None:
+        nbytes = ctypes.c_size_t()
+        _check(lib.e3_group_norm_workspace_size(features.handle, N, B, max_rows, ctypes.byref(nbytes)))
+        if len(features.workspace_bytes) > 4096:
+            features.workspace_bytes.clear()
+        n = features.workspace_bytes[(N, B, max_rows)] = nbytes.value
+    if n == 0:
+        return None, None, 0
+    ws = torch.empty(n, dtype=torch.uint8, device=features.device)
+    return ws, ws.data_ptr(), n
 
 
 def group_norm_forward(features, x, weight=None, bias=None, segments=None, eps=1e-5, act=None, p=0.0, rng=None,
@@ -824,37 +848,35 @@ def group_norm_forward(features, x, weight=None, bias=None, segments=None, eps=1
     """(y, stats): group norm of rows x [N, dim] over the segments (None: one segment of all rows), then
     the activation on the 0e channels, then dropout (e3_group_norm_forward).  ``stats`` [B, n_groups, 2]
     float64 holds (mean, 1 / deviation) for the backward.  Padding rows of y are zero."""
-    N, B, row_ptr, max_rows = _norm_args(features, x, weight, bias, segments, act)
-    spec = _drop_spec(features, p, rng, row0)
+    N, B, row_ptr, max_rows, px, pw, pb = _norm_args(features, x, weight, bias, segments, act)
     if out is None:
         out = torch.empty_like(x)
-    else:
-        _need(out, "out", features.dtype, x.shape, features.device)
     stats = torch.empty((B, features.n_groups, 2), dtype=torch.float64, device=features.device)
-    ws = _norm_workspace(features, N, B, max_rows)
-    _check(lib.e3_group_norm_forward(features.handle, N, B, _ptr(row_ptr), max_rows, _ptr(x), _ptr(weight), _ptr(bias),
-                                     float(eps), _ACTS[act], None if spec is None else ctypes.byref(spec), _ptr(out),
-                                     _ptr(stats), _ptr(ws), ws.numel(), _stream()))
+    ws, pws, n = _norm_workspace(features, N, B, max_rows)
+    _check(lib.e3_group_norm_forward(features.handle, N, B, row_ptr, max_rows, px, pw, pb, eps, _ACTS[act],
+                                     _drop_spec(features, p, rng, row0), _rows(out, "out", features, x.shape),
+                                     stats.data_ptr(), pws, n, _row_stream(features)))
     return out, stats
+
+
+def _norm_stats(features, stats, B):
+    return _need(stats, "stats", torch.float64, (B, features.n_groups, 2), features.device).data_ptr()
 
 
 def group_norm_backward(features, x, stats, grad_y, weight=None, bias=None, segments=None, act=None, p=0.0, rng=None,
                         row0=0, need_x=True, need_weight=True, need_bias=True):
     """(grad_x, grad_weight, grad_bias) of <grad_y, y> (e3_group_norm_backward); skipped ones are None.
     Arguments as the forward's, with its ``stats``."""
-    N, B, row_ptr, max_rows = _norm_args(features, x, weight, bias, segments, act)
+    N, B, row_ptr, max_rows, px, pw, pb = _norm_args(features, x, weight, bias, segments, act)
     dt, dev = features.dtype, features.device
-    _need(stats, "stats", torch.float64, (B, features.n_groups, 2), dev)
-    _need(grad_y, "grad_y", dt, x.shape, dev)
-    spec = _drop_spec(features, p, rng, row0)
     gx = torch.empty_like(x) if need_x else None
     gw = torch.empty(features.n_channels, dtype=dt, device=dev) if need_weight else None
     gb = torch.empty(features.n_scalars, dtype=dt, device=dev) if need_bias else None
-    ws = _norm_workspace(features, N, B, max_rows)
-    _check(lib.e3_group_norm_backward(features.handle, N, B, _ptr(row_ptr), max_rows, _ptr(x), _ptr(stats),
-                                      _ptr(weight), _ptr(bias), _ACTS[act],
-                                      None if spec is None else ctypes.byref(spec), _ptr(grad_y), _ptr(gx), _ptr(gw),
-                                      _ptr(gb), _ptr(ws), ws.numel(), _stream()))
+    ws, pws, n = _norm_workspace(features, N, B, max_rows)
+    _check(lib.e3_group_norm_backward(features.handle, N, B, row_ptr, max_rows, px, _norm_stats(features, stats, B),
+                                      pw, pb, _ACTS[act], _drop_spec(features, p, rng, row0),
+                                      _rows(grad_y, "grad_y", features, x.shape), _ptr(gx), _ptr(gw), _ptr(gb), pws,
+                                      n, _row_stream(features)))
     return gx, gw, gb
 
 
@@ -863,25 +885,21 @@ def group_norm_double_backward(features, x, stats, grad_y, weight=None, bias=Non
                                need_x=True, need_weight=True, need_bias=True):
     """(d_grad_y, d_x, d_weight, d_bias): the backward of ``group_norm_backward`` for upstream gradients
     u_x, u_weight, u_bias of its three results, None being zero (e3_group_norm_double_backward)."""
-    N, B, row_ptr, max_rows = _norm_args(features, x, weight, bias, segments, act)
+    N, B, row_ptr, max_rows, px, pw, pb = _norm_args(features, x, weight, bias, segments, act)
     dt, dev = features.dtype, features.device
-    _need(stats, "stats", torch.float64, (B, features.n_groups, 2), dev)
-    _need(grad_y, "grad_y", dt, x.shape, dev)
-    for t, name, shape in ((u_x, "u_x", x.shape), (u_weight, "u_weight", (features.n_channels,)),
-                           (u_bias, "u_bias", (features.n_scalars,))):
-        if t is not None:
-            _need(t, name, dt, shape, dev)
-    spec = _drop_spec(features, p, rng, row0)
+    pg = _rows(grad_y, "grad_y", features, x.shape)
+    pux = _opt_rows(u_x, "u_x", features, x.shape)
+    puw = _opt_rows(u_weight, "u_weight", features, (features.n_channels,))
+    pub = _opt_rows(u_bias, "u_bias", features, (features.n_scalars,))
     dg = torch.empty_like(x) if need_grad_y else None
     dx = torch.empty_like(x) if need_x else None
     dw = torch.empty(features.n_channels, dtype=dt, device=dev) if need_weight else None
     db = torch.empty(features.n_scalars, dtype=dt, device=dev) if need_bias else None
-    ws = _norm_workspace(features, N, B, max_rows)
-    _check(lib.e3_group_norm_double_backward(features.handle, N, B, _ptr(row_ptr), max_rows, _ptr(x), _ptr(stats),
-                                             _ptr(weight), _ptr(bias), _ACTS[act],
-                                             None if spec is None else ctypes.byref(spec), _ptr(grad_y), _ptr(u_x),
-                                             _ptr(u_weight), _ptr(u_bias), _ptr(dg), _ptr(dx), _ptr(dw), _ptr(db),
-                                             _ptr(ws), ws.numel(), _stream()))
+    ws, pws, n = _norm_workspace(features, N, B, max_rows)
+    _check(lib.e3_group_norm_double_backward(features.handle, N, B, row_ptr, max_rows, px,
+                                             _norm_stats(features, stats, B), pw, pb, _ACTS[act],
+                                             _drop_spec(features, p, rng, row0), pg, pux, puw, pub, _ptr(dg), _ptr(dx),
+                                             _ptr(dw), _ptr(db), pws, n, _row_stream(features)))
     return dg, dx, dw, db
 
 
