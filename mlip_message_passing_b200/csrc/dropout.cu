@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(DR_THREADS) dropout_kernel(const __grid_consta
         const uint32_t keep = DROP ? dc.keep(row) : ~0u;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          const T d = (keep >> j & 1u) ? (DROP ? v[i].v[j] * scale : v[i].v[j]) : T(0);
+          const T d = DropCol<VEC>::kept(keep, j) ? (DROP ? v[i].v[j] * scale : v[i].v[j]) : T(0);
           v[i].v[j] = RES ? d + q[i].v[j] : d;
         }
         store_row<T, VEC>(out + row * D, v[i]);

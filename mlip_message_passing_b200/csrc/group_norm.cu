@@ -94,11 +94,11 @@ GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows,
     t = &f->rows;
     threads = GN_ROW_THREADS;
     a->k = 1;
-    a->j = threads / t->tx;
+    a->j = std::min(threads / t->tx, std::max(1, 128 / t->groups));  // the items' coefficients stay small
   } else if ((int64_t(RP) << shift) >= most && t->n() > 0 && t->n() <= 64) {
     c.local = true;
     a->k = 1 << shift;
-    a->j = std::max(1, GN_THREADS / (t->tx << shift));
+    a->j = std::min(std::max(1, GN_THREADS / (t->tx << shift)), std::max(1, 128 / t->groups));
   }
   // clusters: when one CTA is too small, or when there are so few CTAs that dividing the rows further lets
   // more SMs load them

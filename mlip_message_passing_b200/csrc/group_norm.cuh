@@ -151,7 +151,7 @@ struct GnCol {
   }
   __device__ __forceinline__ uint32_t keep(int row) const { return DROP ? dc.keep(row) : ~0u; }
   __device__ __forceinline__ T drop(uint32_t kp, int i, T v) const {
-    return DROP ? ((kp >> i & 1u) ? v * scale : T(0)) : v;
+    return DROP ? (DropCol<VEC>::kept(kp, i) ? v * scale : T(0)) : v;
   }
   template <int KIND>
   __device__ __forceinline__ T z(const GnStat<T>& st, T x) const {
@@ -601,13 +601,15 @@ __device__ __forceinline__ void gn_join(int E, int lane, int lanes, int stride, 
 
 // ------------------------------------------------------------------------------------- local ---
 // Thread (j, k, tx) owns vector column tx of the CTA's tile and row lane k of segments j, j + J, ..
-// (M of them) of the current batch; R rows of each wait in its slots, while the next batch is on its
-// way into others.  With CL a cluster's CTAs have K row lanes each of one segment; each writes its
+// (M of them) of the current batch; R rows of each wait in its slots, which the next batch takes as
+// soon as they are read the second time.  (A second set of slots, filled a batch ahead, was slower: a batch
+// spends far longer between the barriers than on its way, so shared memory is better spent on more rows.)
+// With CL a cluster's CTAs have K row lanes each of one segment; each writes its
 // sums into the shared memory of all.
 template <typename T, int VEC, int OP, int R, int M, bool CL, int NT>
 struct GnLocal {
   static constexpr int NS = gn_sums(OP), NC = gn_coefs(OP);
-  static constexpr size_t slot_bytes = size_t(2) * R * M * GnSlots<T, VEC, OP, NT>::SLOT;
+  static constexpr size_t slot_bytes = size_t(R) * M * GnSlots<T, VEC, OP, NT>::SLOT;
   static constexpr size_t col_bytes = OP == GN_FWD ? 0 : sizeof(double) * 2 * VEC * NT;
   static constexpr size_t buf_bytes = sizeof(T) * NS * M * NT;
   // sums of a cluster's CTAs, twice: [parity][sum][rank][local group]
@@ -628,25 +630,24 @@ struct GnBatch {
 
 template <int KIND, typename T, int VEC, int OP, bool DROP, int R, int M, int NT>
 __device__ __forceinline__ void gn_local_sums(const GnCol<T, VEC, OP, DROP>& c, const GnStat<T> (&st)[M],
-                                              const GnSlots<T, VEC, OP, NT>& sl, int slot0, const GnBatch<M>& t, int step,
-                                              T* buf, T* cw, T* cb) {
+                                              const GnSlots<T, VEC, OP, NT>& sl, const GnBatch<M>& t, int step, T* buf,
+                                              T* cw, T* cb) {
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     GnAcc<T, VEC, OP, DROP> acc;
     acc.clear(c);
     T piv = T(0);
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (i < t.n[m]) {
-        GnRow<T, VEC> v;
-        sl.read(slot0 + m * R + i, v);
-        if (OP == GN_FWD && KIND != GN_PLAIN && i == 0) piv = v.x.v[0];
-        acc.template add<KIND>(c, st[m], piv, v, t.row0[m] + i * step);
-        if (OP == GN_BWD) {  // z and c for the second pass
-          sl.write(slot0 + m * R + i, 0, v.x);
-          sl.write(slot0 + m * R + i, 1, v.g);
-        }
+    if (OP == GN_FWD && KIND != GN_PLAIN && t.n[m] > 0) piv = sl.get(m * R, 0).v[0];
+#pragma unroll 4
+    for (int i = 0; i < (R == 1 ? min(t.n[m], 1) : t.n[m]); ++i) {
+      GnRow<T, VEC> v;
+      sl.read(m * R + i, v);
+      acc.template add<KIND>(c, st[m], piv, v, t.row0[m] + i * step);
+      if (OP == GN_BWD) {  // z and c for the second pass
+        sl.write(m * R + i, 0, v.x);
+        sl.write(m * R + i, 1, v.g);
       }
+    }
     gn_publish<KIND, OP, T, VEC>(c, acc, piv, t.n[m], buf + m * NT, M * NT);
     if constexpr (OP == GN_BWD) {
 #pragma unroll
@@ -660,7 +661,7 @@ __device__ __forceinline__ void gn_local_sums(const GnCol<T, VEC, OP, DROP>& c, 
 
 template <int KIND, typename T, int VEC, int OP, bool DROP, int R, int M, int NT>
 __device__ __forceinline__ void gn_local_apply(const NormArgs& a, const GnCol<T, VEC, OP, DROP>& c,
-                                               GnStat<T> (&st)[M], const GnSlots<T, VEC, OP, NT>& sl, int slot0,
+                                               GnStat<T> (&st)[M], const GnSlots<T, VEC, OP, NT>& sl,
                                                const GnBatch<M>& t, int step, const T* res, int res_step, T* cw,
                                                T* cb) {
   constexpr int NC = gn_coefs(OP);
@@ -674,14 +675,13 @@ __device__ __forceinline__ void gn_local_apply(const NormArgs& a, const GnCol<T,
       st[m].lo = kf[1];
       st[m].r = kf[2];
     }
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (i < t.n[m]) {
-        const int r = t.row0[m] + i * step;
-        GnRow<T, VEC> v;
-        sl.read(slot0 + m * R + i, v);
-        gn_apply<KIND>(a, c, st[m], kf, v, int64_t(r) * a.lay.dim + c.col, r, cw, cb);
-      }
+#pragma unroll 4
+    for (int i = 0; i < (R == 1 ? min(t.n[m], 1) : t.n[m]); ++i) {
+      const int r = t.row0[m] + i * step;
+      GnRow<T, VEC> v;
+      sl.read(m * R + i, v);
+      gn_apply<KIND>(a, c, st[m], kf, v, int64_t(r) * a.lay.dim + c.col, r, cw, cb);
+    }
   }
 }
 
@@ -730,7 +730,7 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
       }
     }
   };
-  // rows of the batch that lo and hi point to, on their way into the slots of parity `half`
+  // rows of the batch that lo and hi point to, on their way into the slots
   auto fetch = [&](int half, GnBatch<M>& t) {
 #pragma unroll
     for (int m = 0; m < M; ++m) {
@@ -745,12 +745,13 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
       t.n[m] = !active ? 0 : R == 1 ? int(e > s + k) : left > 0 ? int(fast_div(uint32_t(left), div_step)) : 0;
       if (active && tx == 0 && ty == j * K) lens[(half * M + m) * J + j] = e - s;
     }
+    const int64_t hop = int64_t(step) * a.lay.dim * int64_t(sizeof(T));
 #pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (i < t.n[m])
-          sl.fetch((half * M + m) * R + i, (int64_t(t.row0[m] + i * step) * a.lay.dim + col) * int64_t(sizeof(T)));
+    for (int m = 0; m < M; ++m) {
+      int64_t at = (int64_t(t.row0[m]) * a.lay.dim + col) * int64_t(sizeof(T));
+#pragma unroll 4
+      for (int i = 0; i < (R == 1 ? min(t.n[m], 1) : t.n[m]); ++i, at += hop) sl.fetch(m * R + i, at);
+    }
     sl.commit();
   };
   int64_t b0 = int64_t(part) * (J * M);
@@ -778,10 +779,6 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
   int rows_held = 0, parity = 0;
   if (CL) cooperative_groups::this_cluster().sync();  // every CTA of the cluster has started
   for (; b0 < a.B; b0 += hop_b, parity ^= 1) {
-    GnBatch<M> next;
-    fetch(parity ^ 1, next);
-    point(b0 + 2 * hop_b);
-    const int slot0 = parity * R * M;
     GnStat<T> st[M];
     if (OP != GN_FWD) {
 #pragma unroll
@@ -790,11 +787,11 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
         if (t.n[m] > 0) st[m].set(a.stats + 2 * (b * G + c.g));
       }
     }
-    sl.template wait<1>();
-    if (c.kind == GN_PLAIN) gn_local_sums<GN_PLAIN, T, VEC, OP, DROP, R, M, NT>(c, st, sl, slot0, t, step, buf + tid, cw, cb);
+    sl.template wait<0>();
+    if (c.kind == GN_PLAIN) gn_local_sums<GN_PLAIN, T, VEC, OP, DROP, R, M, NT>(c, st, sl, t, step, buf + tid, cw, cb);
     else if (c.kind == GN_CENTRED)
-      gn_local_sums<GN_CENTRED, T, VEC, OP, DROP, R, M, NT>(c, st, sl, slot0, t, step, buf + tid, cw, cb);
-    else gn_local_sums<GN_ACT, T, VEC, OP, DROP, R, M, NT>(c, st, sl, slot0, t, step, buf + tid, cw, cb);
+      gn_local_sums<GN_CENTRED, T, VEC, OP, DROP, R, M, NT>(c, st, sl, t, step, buf + tid, cw, cb);
+    else gn_local_sums<GN_ACT, T, VEC, OP, DROP, R, M, NT>(c, st, sl, t, step, buf + tid, cw, cb);
     __syncthreads();
     // item (m, jj, lg): K row lanes x the group's vectors
     for (int base = 0; base < items; base += per) {
@@ -853,10 +850,10 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
     const T* q = res + NC * ((active ? j : 0) * nlg + c.lg);
     const int hop_res = NC * J * nlg;
     if (c.kind == GN_PLAIN)
-      gn_local_apply<GN_PLAIN, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, slot0, t, step, q, hop_res, cw, cb);
+      gn_local_apply<GN_PLAIN, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, t, step, q, hop_res, cw, cb);
     else if (c.kind == GN_CENTRED)
-      gn_local_apply<GN_CENTRED, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, slot0, t, step, q, hop_res, cw, cb);
-    else gn_local_apply<GN_ACT, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, slot0, t, step, q, hop_res, cw, cb);
+      gn_local_apply<GN_CENTRED, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, t, step, q, hop_res, cw, cb);
+    else gn_local_apply<GN_ACT, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, t, step, q, hop_res, cw, cb);
     rows_held += R * M;
     if (columns && rows_held >= GN_FLUSH) {
       rows_held = 0;
@@ -867,9 +864,9 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
         cw[i] = cb[i] = T(0);
       }
     }
-    t = next;
+    fetch(parity ^ 1, t);
+    point(b0 + 2 * hop_b);
   }
-  sl.template wait<0>();
   if (active)
     gn_zero_rows<T, VEC, OP>(a, c.col, gn_rows_end(a) + int64_t(blockIdx.x) * (J * K) + ty, a.N,
                              int64_t(gridDim.x) * (J * K));

@@ -20,8 +20,8 @@ struct GnConfig {
 };
 // rows that a thread of the local kernel holds; segments that share them when every
 // segment is one row
-__host__ __device__ constexpr int gn_reg_rows(int op) { return op == GN_FWD ? 8 : op == GN_BWD ? 4 : 2; }
-__host__ __device__ constexpr int gn_reg_segments(int op) { return op == GN_FWD ? 4 : op == GN_BWD ? 2 : 1; }
+__host__ __device__ constexpr int gn_reg_rows(int op) { return op == GN_FWD ? 16 : op == GN_BWD ? 8 : 4; }
+__host__ __device__ constexpr int gn_reg_segments(int op) { return op == GN_DBL ? 1 : 4; }
 
 // Chunks and workspace of the grid kernel on `ctas` resident CTAs; returns the bytes needed.
 size_t gn_grid_layout(NormArgs* a, int op, int64_t ctas);

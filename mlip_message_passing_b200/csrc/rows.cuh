@@ -87,7 +87,7 @@ __device__ __forceinline__ uint4 philox10(uint4 c, uint32_t k0, uint32_t k1) {
 template <int VEC>
 struct DropCol {
   uint32_t quad, block;
-  uint32_t sel;  // 2 bits per element
+  uint32_t bytes;  // byte i: 1 << (word of element i)
   uint32_t k0, k1, offset, thr, row0;
 
   __device__ __forceinline__ void init(const RowLayout& L, const DropArgs& a, int col) {
@@ -95,9 +95,9 @@ struct DropCol {
     const uint32_t o = uint32_t(col - L.blk[b].col0);
     block = uint32_t(b);
     quad = fast_div(o, L.blk[b].div_d) >> 2;
-    sel = 0;
+    bytes = 0;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) sel |= (fast_div(o + i, L.blk[b].div_d) & 3u) << (2 * i);
+    for (int i = 0; i < VEC; ++i) bytes |= 1u << ((fast_div(o + i, L.blk[b].div_d) & 3u) + 8 * i);
     k0 = a.k0;
     k1 = a.k1;
     offset = a.offset;
@@ -110,16 +110,14 @@ struct DropCol {
     thr = a.thr;
     row0 = a.row0;
   }
-  // bit i: element i of this column's vector in `row` stays
+  // byte i is not 0: element i of this column's vector in `row` stays
   __device__ __forceinline__ uint32_t keep(int64_t row) const {
     const uint4 w = philox10(make_uint4(quad, row0 + uint32_t(row), block, offset), k0, k1);
     const uint32_t m = uint32_t(w.x >= thr) | uint32_t(w.y >= thr) << 1 | uint32_t(w.z >= thr) << 2 |
                        uint32_t(w.w >= thr) << 3;
-    uint32_t r = 0;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) r |= ((m >> ((sel >> (2 * i)) & 3u)) & 1u) << i;
-    return r;
+    return (m * 0x01010101u) & bytes;
   }
+  static __device__ __forceinline__ bool kept(uint32_t k, int i) { return (k & (0xFFu << (8 * i))) != 0; }
 };
 
 }  // namespace e3b
