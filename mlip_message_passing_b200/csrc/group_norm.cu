@@ -107,11 +107,13 @@ GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows,
     const int k = GN_THREADS / n->tx;
     int cs = 1;
     while (cs < 16 && int64_t(RP) * k * cs < most) cs *= 2;
-    // all clusters at once (in the backwards they meet for the parameters' gradients, on one CTA per SM)
+    // all clusters at once; in the backwards the clusters of a tile meet for the parameters' gradients, so
+    // there they have to be resident (counted as one CTA per SM), unless there is one per tile
     const int64_t all = B * n->n();
-    const bool fits = int64_t(RP) * k * cs >= most && all * cs <= (op == GN_FWD ? 2 * sm_count() : 128);
+    const int64_t room = op == GN_FWD || B == 1 ? 2 * sm_count() : 128;
+    const bool fits = int64_t(RP) * k * cs >= most && all * cs <= room;
     if (fits && (!c.local || (a->j == 1 && int64_t(t->n()) * B < sm_count()))) {
-      while (cs < 8 && all * cs * 2 <= (op == GN_FWD ? 2 * sm_count() : 128) && most > 2 * k * cs) cs *= 2;
+      while (cs < 8 && all * cs * 2 <= room && most > 2 * k * cs) cs *= 2;
       c.local = true;
       t = n;
       a->k = k;

@@ -687,7 +687,7 @@ __device__ __forceinline__ void gn_local_apply(const NormArgs& a, const GnCol<T,
 
 // CTAs that have to fit an SM
 __host__ __device__ constexpr int gn_local_ctas(int op, int threads) {
-  return threads > GN_THREADS ? (op == GN_FWD ? 2 : 1) : op == GN_DBL ? 2 : 3;
+  return threads > GN_THREADS ? (op == GN_FWD ? 2 : 1) : op == GN_FWD ? 3 : 2;
 }
 
 template <typename T, int VEC, int OP, bool DROP, int R, int M, bool CL, int NT>
@@ -877,7 +877,8 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
       colbase[(VEC + i) * NT + tid] += double(cb[i]);
     }
     gn_store_columns<VEC, NT>(a, colbase, int(blockIdx.x), v0, W, a.tx, J * K);
-    cooperative_groups::this_grid().sync();
+    if (CL && parts == 1) cooperative_groups::this_cluster().sync();  // the cluster has the tile to itself
+    else cooperative_groups::this_grid().sync();
     gn_finish_columns<T, VEC, NT>(a, int(gridDim.x), v0, W, int(blockIdx.x), int(gridDim.x));
   }
 }

@@ -110,7 +110,8 @@ e3_status gn_run_local(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s)
       if (dev < 64) clusters[dev][size].store(n, std::memory_order_relaxed);
     }
     room = std::min<int64_t>(room, n / a.n_tiles);
-    if (OP == GN_FWD && n > 0) room = std::max<int64_t>(room, 1);  // nothing here waits for other clusters
+    // nothing waits for other clusters in the forward, nor where one cluster has all of a tile's segments
+    if (n > 0) room = std::max<int64_t>(room, 1);
   }
   if (room < 1) return fail(E3_ERR_CUDA, "group norm: no room for the kernel on this device");
   const int64_t batch = int64_t(a.j) * M;
@@ -118,7 +119,7 @@ e3_status gn_run_local(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s)
   if (gn_local_layout(&a, OP, parts) > c.ws_bytes) return fail(E3_ERR_SHAPE, "group norm: workspace too small");
   const bool columns = OP != GN_FWD && (a.gw != nullptr || a.gb != nullptr);
   a.colpart = columns ? static_cast<double*>(ws) : nullptr;
-  return gn_start(kernel, a, dim3(unsigned(parts), unsigned(a.n_tiles)), smem, columns, a.cs, s, NT);
+  return gn_start(kernel, a, dim3(unsigned(parts), unsigned(a.n_tiles)), smem, columns && !(CL && parts == a.cs), a.cs, s, NT);
 }
 
 template <typename T, int VEC, int OP, bool DROP>
