@@ -971,7 +971,25 @@ def case_uuu(torch, e3b, W, dev):
     return float(out.abs().mean() + gx.abs().mean())
 
 
-KERNEL_CASES = {"radial": case_radial, "uvw": case_uvw, "uuu": case_uuu}
+def case_norm(torch, e3b, W, dev):
+    """Group norm with SiLU and dropout on the large graph's rows (24 000 x 2048, one structure: the grid kernel):
+    2 x (forward, backward); then one normalisation per row (the local kernel) and a dropout with a residual."""
+    cfg = W.CONFIGS["conv_large"]
+    f = e3b.Features(W.irreps_str(cfg["mul"], cfg["lx"]), groups=16)
+    one = e3b.Features(W.irreps_str(cfg["mul"], cfg["lx"]))
+    gen = torch.Generator(device=dev).manual_seed(0)
+    x = torch.randn(cfg["N"], f.dim, generator=gen, device=dev)
+    g = torch.randn(cfg["N"], f.dim, generator=gen, device=dev)
+    rows = e3b.Segments.from_counts([1] * cfg["N"])
+    for i in range(2):
+        y, stats = e3b.group_norm_forward(f, x, act="silu", p=0.1, rng=i)
+        gx, gw, gb = e3b.group_norm_backward(f, x, stats, g, act="silu", p=0.1, rng=i)
+    z, _ = e3b.group_norm_forward(one, x, segments=rows)
+    z = e3b.dropout_forward(one, z, 0.1, 3, residual=x)
+    return float(y.abs().mean() + gx.abs().mean() + z.abs().mean())
+
+
+KERNEL_CASES = {"radial": case_radial, "uvw": case_uvw, "uuu": case_uuu, "norm": case_norm}
 
 
 def run_kernel_case(name):

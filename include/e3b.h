@@ -40,7 +40,7 @@
  *     is available from e3_last_error().  Errors seen on the device (an index out of range,
  *     a bounded wait that gave up) are recorded in a status word: the plan's own for calls
  *     that take a plan (read and cleared by e3_plan_status()), one per device for the others
- *     (CSR, harmonics, radial network); e3_device_status() reads and clears the device's word
+ *     (CSR, harmonics, radial network, group norm); e3_device_status() reads and clears the device's word
  *     and the words of every live plan on the device.  The offending edge is skipped, never
  *     dereferenced.
  *   - Results are deterministic: the same inputs give bitwise the same outputs (no atomics
@@ -389,8 +389,11 @@ typedef enum { E3_ACT_NONE = 0, E3_ACT_SILU = 1 } e3_act;
  *            segment), read by the backward;
  *   workspace  device buffer of e3_group_norm_workspace_size bytes (it covers all three calls; 0: may
  *            be NULL), 16-byte aligned, not used by any other call while this one runs on its stream.
- * Sums run in the rows' type over at most 64 rows of a thread, and over a segment that fits one block
- * of threads; in double from there on.  Their order is fixed: results are bitwise repeatable.  N < 2^31, 1 <= B < 2^31.  N == 0 leaves every row output alone and
+ * Sums run in the rows' type over at most 64 rows of a thread and over the threads, CTAs and chunks of a
+ * segment (means relative to a value of the segment, and kept in double).  Their order is fixed: results
+ * are bitwise repeatable.  The kernels of long segments, and of the parameters' gradients, are
+ * cooperative launches; all calls can be recorded into a CUDA graph (after a first call on the device,
+ * which sets up its status word).  N <= 2^31 - 65536, 1 <= B < 2^31.  N == 0 leaves every row output alone and
  * zero-fills the parameters' gradients. */
 E3_API e3_status e3_group_norm_workspace_size(const e3_features* features, int64_t N, int64_t B, int64_t max_rows,
                                               size_t* bytes);

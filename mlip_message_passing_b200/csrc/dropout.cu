@@ -3,7 +3,10 @@
 // out = keep ? x / (1 - p) : 0 (+ residual).  The mask is a function of (seed, offset, row, block,
 // channel), so nothing but x (and the residual) is read and nothing but out is written: the kernel
 // is bound by HBM.  A thread keeps one 16-byte column of the rows and walks down them, so the place of
-// its column in the irreps layout is worked out once; one generator call serves one vector.
+// its column in the irreps layout is worked out once; one generator call (ten rounds, about 70 instructions)
+// serves one vector.  Measured (B200, float32): 24000 x 2048 with a residual 97 us = 6.1 TB/s (93% of a copy),
+// 1.2 M x 64 scalars 109 us = 5.6 TB/s (86%: one word per value, the generator's instructions show); 400 x 576 in
+// 3.3 us.  Four rows in flight per thread and eight CTAs per SM's worth of chunks keep HBM busy.
 #include <algorithm>
 
 #include "internal.h"

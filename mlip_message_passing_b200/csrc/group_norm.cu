@@ -6,6 +6,9 @@
 namespace e3b {
 namespace {
 
+// Row numbers plus a CTA's row lanes stay below 2^31.
+constexpr int64_t GN_MAX_ROWS = (int64_t(1) << 31) - 65536;
+
 size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 
 void count_groups(const RowLayout& L, int vec, TileSet* t) {
@@ -154,7 +157,7 @@ size_t workspace_bytes_of(const GnConfig& c, NormArgs a, int op) {
 e3_status check_sizes(const e3_features* f, int64_t N, int64_t B, bool one_ok) {
   const e3_status st = check_features_device(f);
   if (st != E3_OK) return st;
-  if (N < 0 || N >= (int64_t(1) << 31)) return fail(E3_ERR_SHAPE, "N = %lld", (long long)N);
+  if (N < 0 || N > GN_MAX_ROWS) return fail(E3_ERR_SHAPE, "N = %lld", (long long)N);
   if (B < 1 || B >= (int64_t(1) << 31)) return fail(E3_ERR_SHAPE, "B = %lld", (long long)B);
   if (!one_ok && B != 1) return fail(E3_ERR_INVALID_ARG, "row_ptr is NULL but B is %lld", (long long)B);
   return E3_OK;
@@ -253,7 +256,7 @@ extern "C" e3_status e3_group_norm_workspace_size(const e3_features* f, int64_t 
                                                   size_t* bytes) {
   clear_error();
   if (f == nullptr || bytes == nullptr) return fail(E3_ERR_INVALID_ARG, "features or bytes is NULL");
-  if (N < 0 || N >= (int64_t(1) << 31) || B < 1 || B >= (int64_t(1) << 31))
+  if (N < 0 || N > GN_MAX_ROWS || B < 1 || B >= (int64_t(1) << 31))
     return fail(E3_ERR_SHAPE, "N = %lld, B = %lld", (long long)N, (long long)B);
   *bytes = 0;
   for (int op = GN_FWD; op <= GN_DBL; ++op) {

@@ -9,17 +9,19 @@ namespace e3b {
 
 static_assert(sizeof(NormArgs) <= 4096, "kernel arguments");
 
-// Threads of a CTA of the local kernel when every segment is one row: rows are wide, batches short.
+// Threads of a CTA of the local kernel when every segment is one row: rows are wide, batches short (256 threads
+// leave a third of them idle on 2048 columns with one group per block).
 constexpr int GN_ROW_THREADS = 512;
 
 struct GnConfig {
   bool local = false;
   bool one_row = false;   // local: no segment has more than one row
-  int64_t max_ctas = 0;   // local: CTAs along the segments that have work
   size_t ws_bytes = 0;
 };
-// rows that a thread of the local kernel holds; segments that share them when every
-// segment is one row
+// Rows of a segment that a thread of the local kernel holds, and segments per thread when every segment is
+// one row: what leaves two or three CTAs to an SM (per thread and row 16, 32, 48 bytes of shared memory).
+// 8, 4 and 2 rows with a second set of slots were slower: 142 us instead of 97 on one-row segments (forward),
+// 113 instead of 92 on molecules (forward and backward).
 __host__ __device__ constexpr int gn_reg_rows(int op) { return op == GN_FWD ? 16 : op == GN_BWD ? 8 : 4; }
 __host__ __device__ constexpr int gn_reg_segments(int op) { return op == GN_DBL ? 1 : 4; }
 
@@ -90,11 +92,12 @@ e3_status gn_run_local(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s)
   const int q = gn_resident(kernel, smem, cache, CL, NT);
   int64_t room = q / a.n_tiles / a.cs;  // clusters along the segments that are resident together
   if (CL) {
-    static std::atomic<int> clusters[64][5];
+    static std::atomic<int64_t> clusters[64][5];  // like gn_resident's cache
     int dev = 0, size = 0;
     cudaGetDevice(&dev);
     while ((1 << size) < a.cs) ++size;
-    int n = dev < 64 ? clusters[dev][size].load(std::memory_order_relaxed) : 0;
+    const int64_t hit = dev < 64 ? clusters[dev][size].load(std::memory_order_relaxed) : 0;
+    int n = hit >> 32 == int64_t(smem) ? int(hit & 0xFFFFFFFF) : 0;
     if (n == 0) {
       cudaLaunchConfig_t cfg{};
       cfg.gridDim = dim3(unsigned(a.cs));
@@ -107,7 +110,7 @@ e3_status gn_run_local(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s)
       cfg.attrs = &attr;
       cfg.numAttrs = 1;
       if (q == 0 || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
-      if (dev < 64) clusters[dev][size].store(n, std::memory_order_relaxed);
+      if (dev < 64) clusters[dev][size].store(int64_t(smem) << 32 | n, std::memory_order_relaxed);
     }
     room = std::min<int64_t>(room, n / a.n_tiles);
     // nothing waits for other clusters in the forward, nor where one cluster has all of a tile's segments

@@ -726,8 +726,8 @@ class Segments:
         n_rows = total if n_rows is None else int(n_rows)
         if total > n_rows:
             raise ValueError(f"counts add up to {total} rows of {n_rows}")
-        if n_rows >= 2 ** 31:
-            raise ValueError("n_rows passes 2^31")
+        if n_rows > 2 ** 31 - 65536:
+            raise ValueError("n_rows passes 2^31 - 65536")
         ptr = torch.zeros(len(counts) + 1, dtype=torch.int32)
         ptr[1:] = torch.tensor(counts, dtype=torch.int64).cumsum(0)
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else device

@@ -355,13 +355,15 @@ def test_rows_beyond_32_bit_offsets(e3b):
 
 # ------------------------------------------------------------------------- run together ---
 
-def test_captured_layer_replays_with_new_masks(e3b):
+@pytest.mark.parametrize("counts", [[20, 0, 700, 30], [20, 9000, 30], [7, 8, 0, 9] * 50, [1] * 300])
+def test_captured_layer_replays_with_new_masks(e3b, counts):
     """norm + dropout, forward and backward, recorded into two CUDA graphs (one layer each) and replayed
-    with another seed: the results of the eager calls."""
+    with another seed: the results of the eager calls.  Clusters, the grid, one CTA, one row each."""
     f = e3b.Features("32x0e+32x1o", groups=4)
-    seg = e3b.Segments.from_counts([20, 0, 700, 30], n_rows=760)
+    n = sum(counts) + 10
+    seg = e3b.Segments.from_counts(counts, n_rows=n)
     gen = torch.Generator(DEV).manual_seed(0)
-    x, g = (torch.randn(760, f.dim, device=DEV, generator=gen) for _ in range(2))
+    x, g = (torch.randn(n, f.dim, device=DEV, generator=gen) for _ in range(2))
     state = torch.tensor([1, 0], dtype=torch.int64, device=DEV)
 
     def layer(src, rng):
@@ -392,6 +394,49 @@ def test_captured_layer_replays_with_new_masks(e3b):
             assert all(torch.equal(u, v) for u, v in zip(got, want))
     e3b.device_status()
     del graphs
+
+
+def test_autograd_defaults_and_changed_state(e3b):
+    """No weight or bias; only some leaves need gradients; a grad that is not contiguous; a third
+    derivative and a state that changed before the backward are refused."""
+    f = e3b.Features("8x0e+4x1o", groups=2, dtype=torch.float64)
+    gen = torch.Generator(DEV).manual_seed(4)
+    x, g = (torch.randn(30, f.dim, device=DEV, dtype=torch.float64, generator=gen) for _ in range(2))
+    seg = e3b.Segments.from_counts([10, 20])
+    leaf = x.clone().requires_grad_(True)
+    y = e3b.group_norm(f, leaf, segments=seg, act="silu")
+    (gx,) = torch.autograd.grad(y, leaf, g.t().contiguous().t(), create_graph=True)
+    _, st = e3b.group_norm_forward(f, x, segments=seg, act="silu")
+    want = e3b.group_norm_backward(f, x, st, g, segments=seg, act="silu")
+    assert torch.equal(gx.detach(), want[0])
+    (dx,) = torch.autograd.grad(gx.square().sum(), leaf, create_graph=True)
+    ref = e3b.group_norm_double_backward(f, x, st, g, u_x=2 * want[0], segments=seg, act="silu")
+    assert torch.equal(dx.detach(), ref[1])
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(dx.sum(), leaf)
+    w = torch.ones(f.n_channels, device=DEV, dtype=torch.float64, requires_grad=True)
+    y = e3b.group_norm(f, x, w, segments=seg)
+    (gw,) = torch.autograd.grad(y, w, g)
+    _, st = e3b.group_norm_forward(f, x, w.detach(), segments=seg)
+    assert torch.equal(gw, e3b.group_norm_backward(f, x, st, g, w.detach(), segments=seg)[1])
+    state = torch.tensor([3, 0], dtype=torch.int64, device=DEV)
+    for call in (lambda: e3b.group_norm(f, leaf, segments=seg, p=0.5, rng=state),
+                 lambda: e3b.dropout(f, leaf, 0.5, state)):
+        y = call()
+        state += 1
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(y, leaf, g)
+
+
+def test_norm_writes_over_its_input(e3b):
+    """out=x: every value is read before it is written, whichever kernel runs."""
+    f = e3b.Features("64x0e+64x1o", groups=8)
+    for counts in ([30] * 20, [1] * 50, [2000], [20_000, 5]):
+        seg = e3b.Segments.from_counts(counts)
+        x = torch.randn(sum(counts), f.dim, device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+        want, _ = e3b.group_norm_forward(f, x, segments=seg, act="silu")
+        y, _ = e3b.group_norm_forward(f, x, segments=seg, act="silu", out=x)
+        assert y is x and torch.equal(x, want)
 
 
 def _box(n, mul, seed):

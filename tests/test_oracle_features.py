@@ -166,9 +166,10 @@ def test_segments_refusals(e3b):
 def test_workspace_size_of_extreme_shapes(e3b):
     nb = ctypes.c_size_t()
     f = e3b.Features("64x0e+64x1o", groups=8)
-    for n, b, m in ((0, 1, 0), (1, 1, 1), (2 ** 31 - 1, 1, 0), (1, 100000, 1), (100000, 100000, 1)):
+    for n, b, m in ((0, 1, 0), (1, 1, 1), (2 ** 31 - 65536, 1, 0), (1, 100000, 1), (100000, 100000, 1)):
         assert e3b.lib.e3_group_norm_workspace_size(f.handle, n, b, m, ctypes.byref(nb)) == e3b.E3_OK
         assert nb.value < 2 ** 33
+    assert e3b.lib.e3_group_norm_workspace_size(f.handle, 2 ** 31 - 65535, 1, 0, ctypes.byref(nb)) == e3b.E3_ERR_SHAPE
     assert e3b.lib.e3_group_norm_workspace_size(f.handle, -1, 1, 0, ctypes.byref(nb)) == e3b.E3_ERR_SHAPE
     assert e3b.lib.e3_group_norm_workspace_size(f.handle, 5, 0, 0, ctypes.byref(nb)) == e3b.E3_ERR_SHAPE
     assert e3b.lib.e3_group_norm_workspace_size(None, 5, 1, 0, ctypes.byref(nb)) == e3b.E3_ERR_INVALID_ARG
