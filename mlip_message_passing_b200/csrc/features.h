@@ -69,5 +69,5 @@ struct e3_features {
   bool cluster_ok = false;       // group norm: the tiles for long segments suit clusters
   int wide = 0;                  // widest group in vectors
   // tiles for 2^i row lanes of a segment, for segments of one row, for clusters, for long segments
-  e3b::TileSet local[9], rows, narrow, grid;
+  e3b::TileSet local[10], rows, narrow, grid;
 };

@@ -86,22 +86,26 @@ GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows,
   a->lay = f->lay;
   const int64_t most = max_rows > 0 ? std::min(max_rows, N) : N;
   const int RP = gn_reg_rows(op);
-  // local: the rows of the longest segment fit one CTA, or a cluster of up to 16
+  // local: the rows of the longest segment fit one CTA's slots, or a cluster of up to 16 CTAs'; or they take
+  // the slots in turns, where there are segments enough to fill the device
   int shift = 0;
-  while ((int64_t(RP) << shift) < most && shift < 8) ++shift;
+  while ((int64_t(RP) << shift) < most && shift < 8 && f->local[shift + 1].n() > 0) ++shift;
   const TileSet* t = &f->local[shift];
-  int threads = GN_THREADS;
   a->cs = 1;
+  a->cap = RP;
+  const bool held = (int64_t(RP) << shift) >= most;
+  const bool turns = (int64_t(GN_FLUSH) << shift) >= most && B * t->n() >= sm_count();
   if (most <= 1 && f->rows.n() > 0 && f->rows.n() <= 64) {
     c.local = c.one_row = true;
     t = &f->rows;
-    threads = GN_ROW_THREADS;
-    a->k = 1;
-    a->j = std::min(threads / t->tx, std::max(1, 128 / t->groups));  // the items' coefficients stay small
-  } else if ((int64_t(RP) << shift) >= most && t->n() > 0 && t->n() <= 64) {
+    a->cap = a->k = 1;
+    // the items' coefficients stay below 2048
+    a->j = std::min(GN_ROW_THREADS / t->tx, std::max(1, 2048 / (gn_reg_segments(op, f->vec) * t->groups)));
+  } else if (t->n() > 0 && t->n() <= 64 && (held || turns)) {
     c.local = true;
+    a->cap = held ? RP : GN_FLUSH;
     a->k = 1 << shift;
-    a->j = std::min(std::max(1, GN_THREADS / (t->tx << shift)), std::max(1, 128 / t->groups));
+    a->j = std::min(std::max(1, GN_THREADS / (t->tx << shift)), std::max(1, 2048 / t->groups));
   }
   // clusters: when one CTA is too small, or when there are so few CTAs that dividing the rows further lets
   // more SMs load them
@@ -115,10 +119,11 @@ GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows,
     const int64_t all = B * n->n();
     const int64_t room = op == GN_FWD || B == 1 ? 2 * sm_count() : 128;
     const bool fits = int64_t(RP) * k * cs >= most && all * cs <= room;
-    if (fits && (!c.local || (a->j == 1 && int64_t(t->n()) * B < sm_count()))) {
+    if (fits && (!c.local || (held && a->j == 1 && int64_t(t->n()) * B < sm_count()))) {
       while (cs < 8 && all * cs * 2 <= room && most > 2 * k * cs) cs *= 2;
       c.local = true;
       t = n;
+      a->cap = RP;
       a->k = k;
       a->j = 1;
       a->cs = cs;
@@ -135,8 +140,15 @@ GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows,
   a->tx = t->tx;
   a->wide = t->cut;
   a->tile_groups = t->groups;
+  // lanes of a join: enough for all entries, but no more than lets every item of a batch have its own at
+  // once, unless that leaves a lane more than 16 entries (one-row segments of 64 columns in 16 groups: 8 lanes
+  // and 32 rounds 336 us, 1 lane and 4 rounds 171 us)
+  const int threads = c.one_row ? GN_ROW_THREADS : GN_THREADS;
+  const int entries = a->k * std::min(f->wide, t->tx);
+  const int items = (c.one_row ? gn_reg_segments(op, f->vec) : 1) * a->j * t->groups;
   a->lanes = 1;
-  while (a->lanes < a->k * std::min(f->wide, t->tx) && a->lanes < 32) a->lanes *= 2;
+  while (a->lanes < 32 && a->lanes < entries && (a->lanes * 2 * items <= threads || a->lanes * 16 < entries))
+    a->lanes *= 2;
   return c;
 }
 
@@ -207,9 +219,10 @@ e3_status zero_params(const e3_features* f, void* gw, void* gb, cudaStream_t s) 
 void make_tiles(e3_features* f) {
   const RowLayout& L = f->lay;
   // 16-byte vectors need every group to be a whole number of them (then every block, and the row, is)
+  // (8 bytes for floats where the groups are even)
   f->vec = f->dtype == E3_F64 ? 2 : 4;
   for (int b = 0; b < L.n_blocks; ++b)
-    if (L.blk[b].group_cols % f->vec != 0) f->vec = 1;
+    while (L.blk[b].group_cols % f->vec != 0) f->vec /= 2;
   for (int b = 0; b < L.n_blocks; ++b) f->wide = std::max(f->wide, L.blk[b].group_cols / f->vec);
   for (int i = 0; i < 9; ++i)
     if ((f->wide << i) <= GN_THREADS)

@@ -72,7 +72,7 @@ struct NormArgs {
   int32_t act;
   int* status;
   int32_t tx, k, j, lanes;  // thread layout: columns, row lanes of a segment, segments, lanes of a join
-  int32_t cs;               // local: CTAs of a cluster
+  int32_t cs, cap;          // local: CTAs of a cluster; rows of a segment that a thread may have
   int32_t wide;             // grid: some group is cut into several tiles
   int32_t n_tiles;          // tiles of columns
   int32_t tile_groups;      // most groups that a tile holds (parts of)
@@ -208,6 +208,13 @@ struct GnSlots {
   template <int N>
   static __device__ __forceinline__ void wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+  }
+  // the vectors at column `col` of rows row, row + step, .. into slots 0 .., waiting for them
+  __device__ __forceinline__ void reload(int row, int n, int step, int dim, int col) const {
+    int64_t at = (int64_t(row) * dim + col) * int64_t(sizeof(T));
+    for (int i = 0; i < n; ++i, at += int64_t(step) * dim * int64_t(sizeof(T))) fetch(i, at);
+    commit();
+    wait<0>();
   }
   __device__ __forceinline__ RowVec<T, VEC> get(int slot, int array) const {
     return load_row<T, VEC>(reinterpret_cast<const T*>(base + slot * SLOT + array * LANE * NT));
@@ -522,10 +529,8 @@ __device__ __forceinline__ void gn_publish(const COL& c, const ACC& acc, T piv, 
 template <typename T>
 __device__ __forceinline__ T gn_lanes_sum(T v, int lanes) {
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2) {
-    const T w = __shfl_xor_sync(~0u, v, o);
-    v += o < lanes ? w : T(0);
-  }
+  for (int o = 16; o > 0; o /= 2)
+    if (o < lanes) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
 
@@ -597,7 +602,8 @@ __device__ __forceinline__ void gn_join(int E, int lane, int lanes, int stride, 
 // (M of them) of the current batch; R rows of each wait in its slots, which the next batch takes as
 // soon as they are read the second time.  (A second set of slots, filled a batch ahead, was slower: a batch
 // spends far longer between the barriers than on its way, so shared memory is better spent on more rows.)
-// With CL a cluster's CTAs have K row lanes each of one segment; each writes its
+// Rows of a thread beyond R, at most GN_FLUSH in all, take the slots in turns and are read again for the
+// second pass, from L2.  With CL a cluster's CTAs have K row lanes each of one segment; each writes its
 // sums into the shared memory of all.
 template <typename T, int VEC, int OP, int R, int M, bool CL, int NT>
 struct GnLocal {
@@ -615,30 +621,46 @@ struct GnLocal {
   }
 };
 
+template <bool V>
+struct GnFlag {
+  static constexpr bool value = V;
+};
+
 // A thread's part of a batch: rows row0[m] + i step, i < n[m].
 template <int M>
 struct GnBatch {
   int row0[M], n[M];
 };
 
-template <int KIND, typename T, int VEC, int OP, bool DROP, int R, int M, int NT>
-__device__ __forceinline__ void gn_local_sums(const GnCol<T, VEC, OP, DROP>& c, const GnStat<T> (&st)[M],
-                                              const GnSlots<T, VEC, OP, NT>& sl, const GnBatch<M>& t, int step, T* buf,
-                                              T* cw, T* cb) {
+template <int KIND, bool TURNS, typename T, int VEC, int OP, bool DROP, int R, int M, int NT>
+__device__ __forceinline__ void gn_local_sums(const NormArgs& a, const GnCol<T, VEC, OP, DROP>& c,
+                                              const GnStat<T> (&st)[M], const GnSlots<T, VEC, OP, NT>& sl,
+                                              const GnBatch<M>& t, int step, T* buf, T* cw, T* cb) {
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     GnAcc<T, VEC, OP, DROP> acc;
     acc.clear(c);
     T piv = T(0);
     if (OP == GN_FWD && KIND != GN_PLAIN && t.n[m] > 0) piv = sl.get(m * R, 0).v[0];
+    auto rows = [&](int row, int n) {
 #pragma unroll 4
-    for (int i = 0; i < (R == 1 ? min(t.n[m], 1) : t.n[m]); ++i) {
-      GnRow<T, VEC> v;
-      sl.read(m * R + i, v);
-      acc.template add<KIND>(c, st[m], piv, v, t.row0[m] + i * step);
-      if (OP == GN_BWD) {  // z and c for the second pass
-        sl.write(m * R + i, 0, v.x);
-        sl.write(m * R + i, 1, v.g);
+      for (int i = 0; i < n; ++i) {
+        GnRow<T, VEC> v;
+        sl.read(m * R + i, v);
+        acc.template add<KIND>(c, st[m], piv, v, row + i * step);
+        if (OP == GN_BWD) {  // z and c for the second pass
+          sl.write(m * R + i, 0, v.x);
+          sl.write(m * R + i, 1, v.g);
+        }
+      }
+    };
+    rows(t.row0[m], min(t.n[m], R));
+    if (TURNS) {
+#pragma unroll 1
+      for (int from = R; from < t.n[m]; from += R) {
+        const int row = t.row0[m] + from * step, n = min(t.n[m] - from, R);
+        sl.reload(row, n, step, a.lay.dim, c.col);
+        rows(row, n);
       }
     }
     gn_publish<KIND, OP, T, VEC>(c, acc, piv, t.n[m], buf + m * NT, M * NT);
@@ -652,7 +674,7 @@ __device__ __forceinline__ void gn_local_sums(const GnCol<T, VEC, OP, DROP>& c, 
   }
 }
 
-template <int KIND, typename T, int VEC, int OP, bool DROP, int R, int M, int NT>
+template <int KIND, bool TURNS, typename T, int VEC, int OP, bool DROP, int R, int M, int NT>
 __device__ __forceinline__ void gn_local_apply(const NormArgs& a, const GnCol<T, VEC, OP, DROP>& c,
                                                GnStat<T> (&st)[M], const GnSlots<T, VEC, OP, NT>& sl,
                                                const GnBatch<M>& t, int step, const T* res, int res_step, T* cw,
@@ -668,12 +690,29 @@ __device__ __forceinline__ void gn_local_apply(const NormArgs& a, const GnCol<T,
       st[m].lo = kf[1];
       st[m].r = kf[2];
     }
+    auto rows = [&](int row, int n, auto again) {
 #pragma unroll 4
-    for (int i = 0; i < (R == 1 ? min(t.n[m], 1) : t.n[m]); ++i) {
-      const int r = t.row0[m] + i * step;
-      GnRow<T, VEC> v;
-      sl.read(m * R + i, v);
-      gn_apply<KIND>(a, c, st[m], kf, v, int64_t(r) * a.lay.dim + c.col, r, cw, cb);
+      for (int i = 0; i < n; ++i) {
+        const int r = row + i * step;
+        GnRow<T, VEC> v;
+        sl.read(m * R + i, v);
+        if constexpr (OP == GN_BWD && again.value) {
+          GnAcc<T, VEC, OP, DROP> z;
+          z.clear(c);
+          z.template add<KIND>(c, st[m], T(0), v, r);
+        }
+        gn_apply<KIND>(a, c, st[m], kf, v, int64_t(r) * a.lay.dim + c.col, r, cw, cb);
+      }
+    };
+    if (!TURNS || t.n[m] <= R) {
+      rows(t.row0[m], min(t.n[m], R), GnFlag<false>{});
+    } else {  // more rows than slots: the first ones are gone
+#pragma unroll 1
+      for (int from = 0; from < t.n[m]; from += R) {
+        const int row = t.row0[m] + from * step, n = min(t.n[m] - from, R);
+        sl.reload(row, n, step, a.lay.dim, c.col);
+        rows(row, n, GnFlag<true>{});
+      }
     }
   }
 }
@@ -688,6 +727,7 @@ __global__ void __launch_bounds__(NT, gn_local_ctas(OP, NT))
 gn_local_kernel(const __grid_constant__ NormArgs a) {
   using L = GnLocal<T, VEC, OP, R, M, CL, NT>;
   constexpr int NS = L::NS, NC = L::NC, STRIDE = M * NT;
+  constexpr bool TURNS = !CL && R > 1;  // a thread may have more rows than slots
   extern __shared__ __align__(16) unsigned char smem[];
   unsigned char* sp = smem + L::slot_bytes;
   double* colbase = reinterpret_cast<double*>(sp);
@@ -728,10 +768,10 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       int s = lo[m], e = hi[m];
-      if (s < 0 || e < s || e > int(a.N) || e - s > R * step) {  // no row pointer, or longer than the caller said
+      if (s < 0 || e < s || e > int(a.N) || e - s > a.cap * step) {  // no row pointer, or longer than the caller said
         atomicCAS(a.status, 0, int(E3_ERR_INDEX));
         s = min(max(s, 0), int(a.N));
-        e = min(min(max(e, s), int(a.N)), s + R * step);
+        e = min(min(max(e, s), int(a.N)), s + a.cap * step);
       }
       t.row0[m] = s + k;
       const int left = e - s - k + step - 1;
@@ -743,7 +783,7 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
     for (int m = 0; m < M; ++m) {
       int64_t at = (int64_t(t.row0[m]) * a.lay.dim + col) * int64_t(sizeof(T));
 #pragma unroll 4
-      for (int i = 0; i < (R == 1 ? min(t.n[m], 1) : t.n[m]); ++i, at += hop) sl.fetch(m * R + i, at);
+      for (int i = 0; i < min(t.n[m], R); ++i, at += hop) sl.fetch(m * R + i, at);
     }
     sl.commit();
   };
@@ -781,10 +821,10 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
       }
     }
     sl.template wait<0>();
-    if (c.kind == GN_PLAIN) gn_local_sums<GN_PLAIN, T, VEC, OP, DROP, R, M, NT>(c, st, sl, t, step, buf + tid, cw, cb);
+    if (c.kind == GN_PLAIN) gn_local_sums<GN_PLAIN, TURNS, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, t, step, buf + tid, cw, cb);
     else if (c.kind == GN_CENTRED)
-      gn_local_sums<GN_CENTRED, T, VEC, OP, DROP, R, M, NT>(c, st, sl, t, step, buf + tid, cw, cb);
-    else gn_local_sums<GN_ACT, T, VEC, OP, DROP, R, M, NT>(c, st, sl, t, step, buf + tid, cw, cb);
+      gn_local_sums<GN_CENTRED, TURNS, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, t, step, buf + tid, cw, cb);
+    else gn_local_sums<GN_ACT, TURNS, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, t, step, buf + tid, cw, cb);
     __syncthreads();
     // item (m, jj, lg): K row lanes x the group's vectors
     for (int base = 0; base < items; base += per) {
@@ -843,10 +883,10 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
     const T* q = res + NC * ((active ? j : 0) * nlg + c.lg);
     const int hop_res = NC * J * nlg;
     if (c.kind == GN_PLAIN)
-      gn_local_apply<GN_PLAIN, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, t, step, q, hop_res, cw, cb);
+      gn_local_apply<GN_PLAIN, TURNS, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, t, step, q, hop_res, cw, cb);
     else if (c.kind == GN_CENTRED)
-      gn_local_apply<GN_CENTRED, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, t, step, q, hop_res, cw, cb);
-    else gn_local_apply<GN_ACT, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, t, step, q, hop_res, cw, cb);
+      gn_local_apply<GN_CENTRED, TURNS, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, t, step, q, hop_res, cw, cb);
+    else gn_local_apply<GN_ACT, TURNS, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, t, step, q, hop_res, cw, cb);
     rows_held += R * M;
     if (columns && rows_held >= GN_FLUSH) {
       rows_held = 0;

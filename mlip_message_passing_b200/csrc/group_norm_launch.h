@@ -23,7 +23,9 @@ struct GnConfig {
 // 8, 4 and 2 rows with a second set of slots were slower: 142 us instead of 97 on one-row segments (forward),
 // 113 instead of 92 on molecules (forward and backward).
 __host__ __device__ constexpr int gn_reg_rows(int op) { return op == GN_FWD ? 16 : op == GN_BWD ? 8 : 4; }
-__host__ __device__ constexpr int gn_reg_segments(int op) { return op == GN_DBL ? 1 : 4; }
+__host__ __device__ constexpr int gn_reg_segments(int op, int vec) {
+  return vec == 1 ? (op == GN_DBL ? 2 : 8) : op == GN_DBL ? 1 : 4;
+}
 
 // Chunks and workspace of the grid kernel on `ctas` resident CTAs; returns the bytes needed.
 size_t gn_grid_layout(NormArgs* a, int op, int64_t ctas);
@@ -128,7 +130,7 @@ e3_status gn_run_local(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s)
 template <typename T, int VEC, int OP, bool DROP>
 e3_status gn_run(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s) {
   if (c.local) {
-    if (c.one_row) return gn_run_local<T, VEC, OP, DROP, 1, gn_reg_segments(OP), false, GN_ROW_THREADS>(a, c, ws, s);
+    if (c.one_row) return gn_run_local<T, VEC, OP, DROP, 1, gn_reg_segments(OP, VEC), false, GN_ROW_THREADS>(a, c, ws, s);
     if (a.cs > 1) return gn_run_local<T, VEC, OP, DROP, gn_reg_rows(OP), 1, true>(a, c, ws, s);
     return gn_run_local<T, VEC, OP, DROP, gn_reg_rows(OP), 1, false>(a, c, ws, s);
   }
@@ -156,6 +158,7 @@ e3_status gn_launch(NormArgs& a, const GnConfig& c, bool f64, int vec, bool drop
     GN_CASE(double, 1);
   }
   if (vec == 4) GN_CASE(float, 4);
+  if (vec == 2) GN_CASE(float, 2);
   GN_CASE(float, 1);
 #undef GN_CASE
 }

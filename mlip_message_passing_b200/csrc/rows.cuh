@@ -35,23 +35,17 @@ __host__ __device__ __forceinline__ uint32_t fast_div(uint32_t x, uint32_t recip
 
 // The same for rows that are not needed again: they leave L2 first.
 template <typename T, int VEC>
-__device__ __forceinline__ RowVec<T, VEC> load_row_last(const T* p) {
-  RowVec<T, VEC> r;
-  if constexpr (sizeof(T) * VEC == 16) {
-    const int4 q = __ldcs(reinterpret_cast<const int4*>(p));
-    memcpy(&r, &q, 16);
-  } else {
-    r.v[0] = __ldcs(p);
-  }
-  return r;
-}
-template <typename T, int VEC>
 __device__ __forceinline__ void store_row_last(T* p, const RowVec<T, VEC>& v) {
-  if constexpr (sizeof(T) * VEC == 16) {
+  if constexpr (sizeof(v) == 16) {
     int4 q;
     memcpy(&q, &v, 16);
     __stcs(reinterpret_cast<int4*>(p), q);
+  } else if constexpr (sizeof(v) == 8) {
+    int2 q;
+    memcpy(&q, &v, 8);
+    __stcs(reinterpret_cast<int2*>(p), q);
   } else {
+    static_assert(VEC == 1, "one vector or one element");
     __stcs(p, v.v[0]);
   }
 }

@@ -85,7 +85,7 @@ def _check_all(e3b, irreps, groups, counts, pad, dtype, act, p, seed, hint="max"
 
 
 LAYOUTS = [("64x0e+64x1o+64x2e", 8), ("128x0e+128x1o", 8), ("64x0e", 8), ("25x0e+7x0o+11x1o+5x2e", 1), ("1x0e", 1),
-           ("4x0e+4x3o", 2), ("3x1o", 3), ("8x1o+8x0e+4x2e+12x0e", 4)]
+           ("4x0e+4x3o", 2), ("3x1o", 3), ("8x1o+8x0e+4x2e+12x0e", 4), ("30x0e+10x1o", 1)]
 
 
 @pytest.mark.parametrize("irreps,groups", LAYOUTS)
@@ -119,6 +119,20 @@ def test_norm_long_segments(e3b, irreps, groups, counts, pad, dtype):
 ])
 def test_norm_hints_and_rows(e3b, irreps, groups, counts, pad, hint):
     _check_all(e3b, irreps, groups, counts, pad, torch.float32, "silu", 0.0, seed=21, hint=hint)
+
+
+@pytest.mark.parametrize("irreps,groups,dtype", [("30x0e+30x1o+30x2e", 1, torch.float32),
+                                                  ("31x0e+7x3o", 1, torch.float32), ("30x0e+30x1o", 1, torch.float64)])
+def test_norm_rows_that_take_turns(e3b, irreps, groups, dtype):
+    """Many segments with more rows than a block's slots: their rows take the slots in turns."""
+    _check_all(e3b, irreps, groups, [60, 3, 41, 0, 64] * 40, 7, dtype, "silu", 0.1, seed=9)
+
+
+def test_norm_many_tiny_rows(e3b):
+    """Rows narrower than a warp, thousands of one-row segments: many segments per block."""
+    _check_all(e3b, "4x0e+4x1o", 4, [1] * 700, 3, torch.float32, "silu", 0.0, seed=9)
+    _check_all(e3b, "1x0e", 1, [1] * 1500, 0, torch.float64, None, 0.0, seed=9)
+    _check_all(e3b, "3x0e+1x1o", 1, [1, 0] * 600, 0, torch.float32, "silu", 0.4, seed=9)
 
 
 def test_norm_bound_that_is_too_small_is_reported(e3b):
