@@ -747,6 +747,15 @@ def _opt_rows(t, name, features, shape):
     return None if t is None else _rows(t, name, features, shape)
 
 
+def _operand(t):
+    """A gradient as the C calls take it: autograd hands over strided ones, and slices of a larger gradient
+    that do not start on a 16-byte boundary."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _row_stream(features):
     """The current stream's handle; the features' device has to be current (the library checks it)."""
     return torch._C._cuda_getCurrentRawStream(features.index)
@@ -801,7 +810,7 @@ class _DropoutFn(torch.autograd.Function):
         rng = ctx.saved_tensors[0] if ctx.saved_tensors else ctx.rng
         gx = None
         if ctx.needs_input_grad[0]:
-            gx = _DropoutFn.apply(g.contiguous(), None, ctx.features, ctx.p, rng, ctx.row0)
+            gx = _DropoutFn.apply(_operand(g), None, ctx.features, ctx.p, rng, ctx.row0)
         return gx, g if ctx.has_residual else None, None, None, None, None
 
 
@@ -903,10 +912,6 @@ def group_norm_double_backward(features, x, stats, grad_y, weight=None, bias=Non
     return dg, dx, dw, db
 
 
-def _contiguous(t):
-    return None if t is None else t.contiguous()
-
-
 class _NormFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, features, segments, eps, act, p, rng, row0):
@@ -919,7 +924,7 @@ class _NormFn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         x, weight, bias, stats, rng = ctx.saved_tensors
-        gx, gw, gb = _NormBwdFn.apply(x, weight, bias, g.contiguous(), stats, ctx.features,
+        gx, gw, gb = _NormBwdFn.apply(x, weight, bias, _operand(g), stats, ctx.features,
                                       ctx.rng if rng is None else rng, tuple(ctx.needs_input_grad[:3]), ctx.kw)
         return gx, gw, gb, None, None, None, None, None, None, None
 
@@ -941,8 +946,8 @@ class _NormBwdFn(torch.autograd.Function):
         x, weight, bias, g, stats, rng = ctx.saved_tensors
         nx, nw, nb, ng = ctx.needs_input_grad[:4]
         dg, dx, dw, db = group_norm_double_backward(
-            ctx.features, x, stats, g, weight, bias, u_x=_contiguous(ux), u_weight=_contiguous(uw),
-            u_bias=_contiguous(ub), rng=ctx.rng if rng is None else rng, need_grad_y=ng, need_x=nx, need_weight=nw,
+            ctx.features, x, stats, g, weight, bias, u_x=_operand(ux), u_weight=_operand(uw),
+            u_bias=_operand(ub), rng=ctx.rng if rng is None else rng, need_grad_y=ng, need_x=nx, need_weight=nw,
             need_bias=nb, **ctx.kw)
         return dx, dw, db, dg, None, None, None, None, None
 

@@ -502,3 +502,26 @@ def test_layer_with_convolution_force_training(e3b):
         want, got = (num[0] - num[1]) / (2 * h), float((grads[i] * u).sum())
         assert abs(got - want) <= 1e-5 * max(1.0, abs(want), float(grads[i].abs().max())), i
     e3b.device_status()
+
+
+def test_gradients_that_start_off_a_vector_boundary(e3b):
+    """The gradient of a concatenation is a slice that starts anywhere: 6 floats into a buffer here."""
+    f = e3b.Features("3x0e+1x1o")
+    gen = torch.Generator(DEV).manual_seed(4)
+    first, x, res = (torch.randn(n, f.dim, device=DEV, generator=gen, requires_grad=True) for n in (1, 5, 5))
+    coef = torch.randn(6, f.dim, device=DEV, generator=gen)
+
+    def run(op, join):
+        y = op()
+        loss = (torch.cat([first, y]) * coef).sum() if join else (y * coef[1:].clone()).sum()
+        (gx,) = torch.autograd.grad(loss + (y ** 2).sum(), x, create_graph=True)
+        return gx.detach(), torch.autograd.grad((torch.cat([first, gx]) * coef).sum() if join
+                                                else (gx * coef[1:].clone()).sum(), x, allow_unused=True)[0]
+
+    for op in (lambda: e3b.group_norm(f, x, act="silu"), lambda: e3b.dropout(f, x, 0.3, 5, residual=res)):
+        for got, want in zip(run(op, True), run(op, False)):
+            assert torch.equal(got, want)
+    y = e3b.group_norm(f, x)
+    (gx,) = torch.autograd.grad((torch.cat([first, y]) * coef).sum(), x)  # the slice itself, added to nothing
+    want, _, _ = e3b.group_norm_backward(f, x.detach(), e3b.group_norm_forward(f, x.detach())[1], coef[1:].clone())
+    assert torch.equal(gx, want)
