@@ -56,6 +56,7 @@ struct TileSet {
   int tx = 0, groups = 0;      // widest tile, most groups of a tile
   bool cut = false;            // some group lies in several tiles
   std::vector<int32_t> first;  // first vector column of each tile, then the end
+  std::vector<int32_t> scalars;  // vector columns of even scalars in each tile
   int n() const { return int(first.size()) - 1; }
 };
 

@@ -17,6 +17,9 @@ void count_groups(const RowLayout& L, int vec, TileSet* t) {
     t->tx = std::max(t->tx, t->first[i + 1] - t->first[i]);
     t->groups = std::max(t->groups, group_of(L, b) - group_of(L, a) + 1);
     if (i > 0 && group_of(L, a - 1) == group_of(L, a)) t->cut = true;
+    int32_t scalars = 0;
+    for (int c = a; c <= b; c += vec) scalars += L.blk[block_of(L, c)].bias0 >= 0;
+    t->scalars.push_back(scalars);
   }
 }
 
@@ -95,13 +98,13 @@ GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows,
   a->cap = RP;
   const bool held = (int64_t(RP) << shift) >= most;
   const bool turns = (int64_t(GN_FLUSH) << shift) >= most && B * t->n() >= sm_count();
-  if (most <= 1 && f->rows.n() > 0 && f->rows.n() <= 64) {
+  if (most <= 1 && f->rows.n() > 0 && f->rows.n() <= GN_LOCAL_TILES) {
     c.local = c.one_row = true;
     t = &f->rows;
     a->cap = a->k = 1;
     // the items' coefficients stay below 2048
     a->j = std::min(GN_ROW_THREADS / t->tx, std::max(1, 2048 / (gn_reg_segments(op, f->vec) * t->groups)));
-  } else if (t->n() > 0 && t->n() <= 64 && (held || turns)) {
+  } else if (t->n() > 0 && t->n() <= GN_LOCAL_TILES && (held || turns)) {
     c.local = true;
     a->cap = held ? RP : GN_FLUSH;
     a->k = 1 << shift;
@@ -137,6 +140,7 @@ GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows,
   }
   std::copy(t->first.begin(), t->first.end(), a->tile);
   a->n_tiles = t->n();
+  c.tiles = t;
   a->tx = t->tx;
   a->wide = t->cut;
   a->tile_groups = t->groups;
@@ -160,9 +164,9 @@ e3_status check_workspace(const void* ws, size_t bytes, size_t need) {
   return E3_OK;
 }
 
-size_t workspace_bytes_of(const GnConfig& c, NormArgs a, int op) {
+size_t workspace_bytes_of(const GnConfig& c, NormArgs a, int op, int vec) {
   const int64_t ctas = int64_t(GN_MAX_RESIDENT) * sm_count();
-  if (c.local) return gn_local_layout(&a, op, std::max<int64_t>(1, ctas / a.n_tiles));
+  if (c.local) return gn_local_layout(a, op, vec, std::max(ctas, int64_t(a.n_tiles) * a.cs));
   return gn_grid_layout(&a, op, ctas);
 }
 
@@ -198,7 +202,7 @@ e3_status begin(const e3_features* f, int64_t N, int64_t B, const int32_t* row_p
   if ((st = drop_args(drop, N, &a->drop, drop_on)) != E3_OK) return st;
   *c = configure(f, N, B, max_rows, op, a);
   c->ws_bytes = ws_bytes;
-  if (N > 0 && (st = check_workspace(ws, ws_bytes, workspace_bytes_of(*c, *a, op))) != E3_OK) return st;
+  if (N > 0 && (st = check_workspace(ws, ws_bytes, workspace_bytes_of(*c, *a, op, f->vec))) != E3_OK) return st;
   if ((st = ensure_device_tables()) != E3_OK) return st;
   if ((st = device_status_ptr(&a->status)) != E3_OK) return st;
   a->row_ptr = row_ptr;
@@ -232,7 +236,7 @@ void make_tiles(e3_features* f) {
   // narrow tiles for clusters, which leave the CTAs more row lanes
   if (f->wide <= 64) f->narrow = cut_tiles(L, f->vec, std::max(f->wide, 8));
   // clusters: few tiles, none with more groups than a CTA's table of its cluster's sums holds
-  f->cluster_ok = f->narrow.n() > 0 && f->narrow.n() <= 64 && f->narrow.groups <= 32;
+  f->cluster_ok = f->narrow.n() > 0 && f->narrow.n() <= GN_LOCAL_TILES && f->narrow.groups <= 32;
 }
 
 // Bytes that a CTA reads for one part of the second pass (64 to 512 KB: 110 to 107 us for the forward of
@@ -257,8 +261,46 @@ size_t gn_grid_layout(NormArgs* a, int op, int64_t ctas) {
   return tickets + al256(size_t(a->n_tiles) * 4);
 }
 
-size_t gn_local_layout(NormArgs* a, int op, int64_t parts) {
-  return op == GN_FWD ? 0 : al256(size_t(parts) * 2 * size_t(a->lay.dim) * 8);
+size_t gn_local_layout(const NormArgs& a, int op, int vec, int64_t ctas) {
+  return op == GN_FWD ? 0 : al256(size_t(ctas) * 2 * size_t(a.tx) * size_t(vec) * 8);
+}
+
+// Even scalars with the activation take a batch half as long again (three quarters in the double backward);
+// without it an eighth.  Every tile the same number of CTAs left some SMs with four times the instructions of
+// others: 512 molecules of 34 rows x 512 columns, forward 32.0 to 29.6 us, backward 53.5 to 51.3, double
+// backward 116 to 103; scalars at twice a batch: 34.2, 54.8, 111.
+void gn_share(NormArgs* a, int op, const TileSet& t, int64_t batches, int64_t room) {
+  const int n = t.n();
+  const double extra = a->act != E3_ACT_SILU ? 0.125 : op == GN_DBL ? 0.75 : 0.5;
+  auto cost = [&](int i) { return t.tx + extra * t.scalars[i]; };
+  auto parts = [&](int i, double limit) {
+    const double each = std::max(1.0, std::floor(limit / cost(i)));  // batches that a CTA does by the limit
+    return std::max<int64_t>(1, std::min(batches, int64_t(std::ceil(double(batches) / each))));
+  };
+  auto total = [&](double limit) {
+    int64_t s = 0;
+    for (int i = 0; i < n; ++i) s += parts(i, limit);
+    return s;
+  };
+  double hi = 0.0, lo = 0.0;  // the limit lies in (lo, hi]
+  for (int i = 0; i < n; ++i) hi = std::max(hi, cost(i));
+  if (total(hi) > room) {
+    lo = hi;
+    hi *= double(batches);
+    for (int i = 0; i < 16 && hi > 1.01 * lo; ++i) {
+      const double mid = std::sqrt(lo * hi);
+      (total(mid) > room ? lo : hi) = mid;
+    }
+  }
+  // what is left over goes to all of them
+  const int64_t used = total(hi), left = std::max<int64_t>(0, room - used);
+  a->start[0] = 0;
+  a->even = 1;
+  for (int i = 0; i < n; ++i) {
+    const int64_t p = parts(i, hi);
+    a->start[i + 1] = a->start[i] + int32_t(std::min(batches, p + p * left / used)) * a->cs;
+    if (a->start[i + 1] != (i + 1) * a->start[1]) a->even = 0;
+  }
 }
 
 }  // namespace e3b
@@ -275,7 +317,7 @@ extern "C" e3_status e3_group_norm_workspace_size(const e3_features* f, int64_t 
   for (int op = GN_FWD; op <= GN_DBL; ++op) {
     NormArgs a{};
     const GnConfig c = configure(f, N, B, max_rows, op, &a);
-    *bytes = std::max(*bytes, workspace_bytes_of(c, a, op));
+    *bytes = std::max(*bytes, workspace_bytes_of(c, a, op, f->vec));
   }
   return E3_OK;
 }

@@ -20,7 +20,7 @@
 //          tiles, meet, join them, meet, and read their rows again.
 // Measured (B200, float32, one call): local, 24000 one-row segments of 2048 columns, forward 97 us = 4.1 TB/s
 // (62% of a copy): two CTAs of 512 threads, bound by the chain from barrier to barrier; 512 segments of 34 rows x
-// 512 columns with dropout, forward 32 us and backward 53 us.  Grid, one segment of 24000 x 2048: forward 107 us
+// 512 columns with dropout, forward 29 us and backward 51 us.  Grid, one segment of 24000 x 2048: forward 107 us
 // (590 MB in three passes, 5.5 TB/s), backward 190 us with dropout (983 MB, 5.2 TB/s).
 // Tried for the grid kernel and dropped: slabs of columns small enough for L2, one after another (24, 50, 100 MB:
 // forward 197, 152, 136 us; a meeting and a join per slab, and narrow tiles, cost more than the re-read; L2 also keeps
@@ -48,6 +48,7 @@ namespace e3b {
 constexpr int GN_THREADS = 256;
 constexpr int GN_FLUSH = 64;     // rows that a thread sums in the rows' type
 constexpr int GN_MAXTILE = 512;  // column tiles at most
+constexpr int GN_LOCAL_TILES = 64;  // of the local kernel
 enum GnOp { GN_FWD = 0, GN_BWD = 1, GN_DBL = 2 };
 // sums of a (segment, group): forward (pivot, mean - pivot, sum of squares around the mean, count),
 // backward (sum c, sum c z), double backward 12
@@ -67,7 +68,7 @@ struct NormArgs {
   double* stats;           // [B][groups][2]
   void* part;              // grid: partial sums, see gn_slot
   void* coef;              // grid: [B][groups][coefs] (backwards)
-  double* colpart;         // [parts][2][dim]: sums for gw, gb per column (NULL: not wanted)
+  double* colpart;         // sums for gw, gb per column, by CTA (NULL: not wanted)
   double eps;
   int32_t act;
   int* status;
@@ -83,6 +84,9 @@ struct NormArgs {
   DropArgs drop;
   RowLayout lay;
   int32_t tile[GN_MAXTILE + 1];  // first vector column of each tile
+  int32_t start[GN_LOCAL_TILES + 1];  // local: first CTA of each tile
+  int32_t even;                       // local: all tiles have the same number of CTAs (blockIdx.y: the tile)
+  int32_t meet;                       // local: the grid meets for the parameters' gradients
 };
 
 // Rows [s, e) of segment b, clamped into [0, N); a bad row pointer is recorded.
@@ -434,28 +438,29 @@ __device__ __forceinline__ void gn_zero_rows(const NormArgs& a, int col, int64_t
 }
 
 // Column sums of a CTA: thread slots colacc[2 VEC][threads] (weights, then biases) added over the row
-// lanes of a column into slot `part` of colpart.  All threads call it.
+// lanes of a column into `out` (weights; biases `apart` further on).  All threads call it.
 template <int VEC, int NT = GN_THREADS>
-__device__ __forceinline__ void gn_store_columns(const NormArgs& a, const double* colacc, int part, int v0, int W,
-                                                 int TX, int TY) {
+__device__ __forceinline__ void gn_store_columns(const double* colacc, double* out, int64_t apart, int W, int TX,
+                                                 int TY) {
   __syncthreads();
   for (int q = int(threadIdx.x); q < 2 * VEC * W; q += NT) {
     const int which = q / (VEC * W), cc = q % (VEC * W), tx = cc / VEC, i = cc % VEC;
     const double* p = colacc + (which * VEC + i) * NT + tx;
     double s = 0.0;
     for (int y = 0; y < TY; ++y) s += p[y * TX];
-    a.colpart[(2 * int64_t(part) + which) * a.lay.dim + v0 * VEC + cc] = s;
+    out[which * apart + cc] = s;
   }
   __syncthreads();
 }
 
-// Gradients of the weights and biases of a tile's channels from the column sums of all `parts` CTAs, after
-// the grid has met; CTA `rank` of `ranks` takes its share.  A tile holds whole channels.
+// Gradients of the weights and biases of a tile's channels from the column sums of its `parts` CTAs (2 `apart`
+// between CTAs), after they have met; CTA `rank` takes its share.  A tile holds whole channels.
 template <typename T, int VEC, int NT = GN_THREADS>
-__device__ __forceinline__ void gn_finish_columns(const NormArgs& a, int parts, int v0, int W, int rank, int ranks) {
+__device__ __forceinline__ void gn_finish_columns(const NormArgs& a, const double* sums, int64_t apart, int parts,
+                                                  int v0, int W, int rank) {
   constexpr int WARPS = NT / 32;
   const int lane = int(threadIdx.x) % 32, n = W * VEC;
-  for (int q = rank * WARPS + int(threadIdx.x) / 32; q < n; q += ranks * WARPS) {
+  for (int q = rank * WARPS + int(threadIdx.x) / 32; q < n; q += parts * WARPS) {
     const int col = v0 * VEC + q;
     const RowBlock& b = a.lay.blk[block_of(a.lay, col)];
     const int u = int(fast_div(uint32_t(col - b.col0), b.div_d));
@@ -463,9 +468,9 @@ __device__ __forceinline__ void gn_finish_columns(const NormArgs& a, int parts, 
     const bool bias = b.bias0 >= 0 && a.gb != nullptr;
     double sw = 0.0, sb = 0.0;
     for (int p = lane; p < parts; p += 32) {
-      const double* r = a.colpart + 2 * int64_t(p) * a.lay.dim + col;
+      const double* r = sums + 2 * int64_t(p) * apart + q;
       for (int m = 0; m < b.d; ++m) sw += __ldcg(r + m);
-      if (bias) sb += __ldcg(r + a.lay.dim);
+      if (bias) sb += __ldcg(r + apart);
     }
     for (int o = 16; o > 0; o /= 2) {
       sw += __shfl_xor_sync(~0u, sw, o);
@@ -736,11 +741,17 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
   T* res = reinterpret_cast<T*>(sp + L::col_bytes + L::buf_bytes + L::all_bytes);
   GnRange* gs = reinterpret_cast<GnRange*>(res + NC * M * a.j * a.tile_groups);
   int* lens = reinterpret_cast<int*>(gs + a.tile_groups);  // rows of a batch's segments: [parity][M J]
-  const int CS = CL ? a.cs : 1, rank = CL ? int(blockIdx.x) % CS : 0;
-  const int part = CL ? int(blockIdx.x) / CS : int(blockIdx.x), parts = CL ? int(gridDim.x) / CS : int(gridDim.x);
+  // this CTA among its tile's (a cluster's CTAs are neighbours, and tiles start with a cluster)
+  int tile = int(blockIdx.y), at = int(blockIdx.x), ctas = int(gridDim.x);
+  if (!a.even) {
+    for (tile = 0; int(blockIdx.x) >= a.start[tile + 1];) ++tile;
+    at = int(blockIdx.x) - a.start[tile];
+    ctas = a.start[tile + 1] - a.start[tile];
+  }
+  const int CS = CL ? a.cs : 1, rank = CL ? at % CS : 0, part = CL ? at / CS : at, parts = CL ? ctas / CS : ctas;
   const int tid = int(threadIdx.x), tx = tid % a.tx, ty = tid / a.tx;
   const int K = a.k, step = K * CS, J = a.j;
-  const int v0 = a.tile[blockIdx.y], W = a.tile[blockIdx.y + 1] - v0;
+  const int v0 = a.tile[tile], W = a.tile[tile + 1] - v0;
   const int j = ty / K, k = rank * K + ty - j * K;
   const bool active = tx < W && j < J;
   const int64_t G = a.lay.n_groups();
@@ -901,18 +912,19 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
     point(b0 + 2 * hop_b);
   }
   if (active)
-    gn_zero_rows<T, VEC, OP>(a, c.col, gn_rows_end(a) + int64_t(blockIdx.x) * (J * K) + ty, a.N,
-                             int64_t(gridDim.x) * (J * K));
+    gn_zero_rows<T, VEC, OP>(a, c.col, gn_rows_end(a) + int64_t(at) * (J * K) + ty, a.N, int64_t(ctas) * (J * K));
   if (columns) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       colbase[i * NT + tid] += double(cw[i]);
       colbase[(VEC + i) * NT + tid] += double(cb[i]);
     }
-    gn_store_columns<VEC, NT>(a, colbase, int(blockIdx.x), v0, W, a.tx, J * K);
-    if (CL && parts == 1) cooperative_groups::this_cluster().sync();  // the cluster has the tile to itself
+    const int apart = a.tx * VEC;
+    double* sums = a.colpart + 2 * int64_t(a.start[tile]) * apart;
+    gn_store_columns<VEC, NT>(colbase, sums + 2 * int64_t(at) * apart, apart, W, a.tx, J * K);
+    if (CL && !a.meet) cooperative_groups::this_cluster().sync();  // every tile has one cluster
     else cooperative_groups::this_grid().sync();
-    gn_finish_columns<T, VEC, NT>(a, int(gridDim.x), v0, W, int(blockIdx.x), int(gridDim.x));
+    gn_finish_columns<T, VEC, NT>(a, sums, apart, ctas, v0, W, at);
   }
 }
 
@@ -1201,7 +1213,8 @@ __global__ void __launch_bounds__(GN_THREADS, OP == GN_FWD ? 3 : 2) gn_grid_kern
     }
     __syncthreads();
   }
-  if (OP == GN_BWD && col_sums) gn_store_columns<VEC>(a, columns, rc, v0, W, a.tx, K);
+  double* csum = col_sums ? a.colpart + v0 * VEC : nullptr;  // [chunk][weights, biases][dim]
+  if (OP == GN_BWD && col_sums) gn_store_columns<VEC>(columns, csum + 2 * rc * int64_t(a.lay.dim), a.lay.dim, W, a.tx, K);
   if (rc == 0 && tid == 0) a.tickets[tile] = a.chunks;  // the first parts are handed out already
   auto grid = cooperative_groups::this_grid();
   grid.sync();
@@ -1265,7 +1278,7 @@ __global__ void __launch_bounds__(GN_THREADS, OP == GN_FWD ? 3 : 2) gn_grid_kern
   bounds();
   p.b = first;
   there = lo < hi && open(true);  // the first rows are on their way while the grid meets
-  if (OP == GN_BWD && col_sums) gn_finish_columns<T, VEC>(a, a.chunks, v0, W, rc, a.chunks);
+  if (OP == GN_BWD && col_sums) gn_finish_columns<T, VEC>(a, csum, a.lay.dim, a.chunks, v0, W, rc);
   grid.sync();
 
   while (true) {
@@ -1296,9 +1309,9 @@ __global__ void __launch_bounds__(GN_THREADS, OP == GN_FWD ? 3 : 2) gn_grid_kern
     there = lo < hi && open(true);
   }
   if (OP == GN_DBL && col_sums) {
-    gn_store_columns<VEC>(a, columns, rc, v0, W, a.tx, K);
+    gn_store_columns<VEC>(columns, csum + 2 * rc * int64_t(a.lay.dim), a.lay.dim, W, a.tx, K);
     grid.sync();
-    gn_finish_columns<T, VEC>(a, a.chunks, v0, W, rc, a.chunks);
+    gn_finish_columns<T, VEC>(a, csum, a.lay.dim, a.chunks, v0, W, rc);
   }
 }
 

@@ -16,6 +16,7 @@ constexpr int GN_ROW_THREADS = 512;
 struct GnConfig {
   bool local = false;
   bool one_row = false;   // local: no segment has more than one row
+  const TileSet* tiles = nullptr;
   size_t ws_bytes = 0;
 };
 // Rows of a segment that a thread of the local kernel holds, and segments per thread when every segment is
@@ -29,7 +30,9 @@ __host__ __device__ constexpr int gn_reg_segments(int op, int vec) {
 
 // Chunks and workspace of the grid kernel on `ctas` resident CTAs; returns the bytes needed.
 size_t gn_grid_layout(NormArgs* a, int op, int64_t ctas);
-size_t gn_local_layout(NormArgs* a, int op, int64_t parts);
+size_t gn_local_layout(const NormArgs& a, int op, int vec, int64_t ctas);
+// Shares out `room` resident CTAs (clusters) among the tiles of the local kernel, `batches` of segments each.
+void gn_share(NormArgs* a, int op, const TileSet& t, int64_t batches, int64_t room);
 // Most CTAs that any kernel here keeps resident on an SM (sizes workspaces).
 constexpr int GN_MAX_RESIDENT = 8;
 
@@ -92,7 +95,7 @@ e3_status gn_run_local(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s)
   const size_t smem = GnLocal<T, VEC, OP, R, M, CL, NT>::smem(a);
   auto kernel = gn_local_kernel<T, VEC, OP, DROP, R, M, CL, NT>;
   const int q = gn_resident(kernel, smem, cache, CL, NT);
-  int64_t room = q / a.n_tiles / a.cs;  // clusters along the segments that are resident together
+  int64_t room = q / a.cs;  // CTAs, or clusters, that are resident together
   if (CL) {
     static std::atomic<int64_t> clusters[64][5];  // like gn_resident's cache
     int dev = 0, size = 0;
@@ -114,17 +117,20 @@ e3_status gn_run_local(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s)
       if (q == 0 || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
       if (dev < 64) clusters[dev][size].store(int64_t(smem) << 32 | n, std::memory_order_relaxed);
     }
-    room = std::min<int64_t>(room, n / a.n_tiles);
+    room = std::min<int64_t>(room, n);
     // nothing waits for other clusters in the forward, nor where one cluster has all of a tile's segments
-    if (n > 0) room = std::max<int64_t>(room, 1);
+    if (n > 0) room = std::max<int64_t>(room, a.n_tiles);
   }
-  if (room < 1) return fail(E3_ERR_CUDA, "group norm: no room for the kernel on this device");
+  if (room < a.n_tiles) return fail(E3_ERR_CUDA, "group norm: no room for the kernel on this device");
   const int64_t batch = int64_t(a.j) * M;
-  const int64_t parts = std::min<int64_t>((a.B + batch - 1) / batch, room) * a.cs;
-  if (gn_local_layout(&a, OP, parts) > c.ws_bytes) return fail(E3_ERR_SHAPE, "group norm: workspace too small");
+  gn_share(&a, OP, *c.tiles, (a.B + batch - 1) / batch, room);
+  const int64_t ctas = a.start[a.n_tiles];
+  if (gn_local_layout(a, OP, VEC, ctas) > c.ws_bytes) return fail(E3_ERR_SHAPE, "group norm: workspace too small");
   const bool columns = OP != GN_FWD && (a.gw != nullptr || a.gb != nullptr);
   a.colpart = columns ? static_cast<double*>(ws) : nullptr;
-  return gn_start(kernel, a, dim3(unsigned(parts), unsigned(a.n_tiles)), smem, columns && !(CL && parts == a.cs), a.cs, s, NT);
+  a.meet = columns && !(CL && ctas == int64_t(a.n_tiles) * a.cs);
+  const dim3 grid = a.even ? dim3(unsigned(a.start[1]), unsigned(a.n_tiles)) : dim3(unsigned(ctas));
+  return gn_start(kernel, a, grid, smem, a.meet != 0, a.cs, s, NT);
 }
 
 template <typename T, int VEC, int OP, bool DROP>

@@ -135,6 +135,14 @@ def test_norm_many_tiny_rows(e3b):
     _check_all(e3b, "3x0e+1x1o", 1, [1, 0] * 600, 0, torch.float32, "silu", 0.4, seed=9)
 
 
+@pytest.mark.parametrize("irreps,groups", [("64x0e+64x1o+64x2e", 8), ("40x0e+40x1o", 4)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float64])
+@pytest.mark.parametrize("act", [None, "silu"])
+def test_norm_more_segments_than_blocks(e3b, irreps, groups, dtype, act):
+    """Tiles of scalars take longer, so they get more blocks: every tile's share is another number."""
+    _check_all(e3b, irreps, groups, [1 + i % 7 for i in range(1500)], 5, dtype, act, 0.2, seed=9)
+
+
 def test_norm_bound_that_is_too_small_is_reported(e3b):
     """Rows of a segment beyond what the bound selected are skipped and the status word says so."""
     f = e3b.Features("8x0e+8x1o", groups=2)
