@@ -17,8 +17,13 @@ void count_groups(const RowLayout& L, int vec, TileSet* t) {
     t->tx = std::max(t->tx, t->first[i + 1] - t->first[i]);
     t->groups = std::max(t->groups, group_of(L, b) - group_of(L, a) + 1);
     if (i > 0 && group_of(L, a - 1) == group_of(L, a)) t->cut = true;
+  }
+}
+
+void count_scalars(const RowLayout& L, int vec, TileSet* t) {
+  for (int i = 0; i < t->n(); ++i) {
     int32_t scalars = 0;
-    for (int c = a; c <= b; c += vec) scalars += L.blk[block_of(L, c)].bias0 >= 0;
+    for (int v = t->first[i]; v < t->first[i + 1]; ++v) scalars += L.blk[block_of(L, v * vec)].bias0 >= 0;
     t->scalars.push_back(scalars);
   }
 }
@@ -235,6 +240,9 @@ void make_tiles(e3_features* f) {
   f->grid = equal_tiles(L, f->vec);
   // narrow tiles for clusters, which leave the CTAs more row lanes
   if (f->wide <= 64) f->narrow = cut_tiles(L, f->vec, std::max(f->wide, 8));
+  for (TileSet& t : f->local) count_scalars(L, f->vec, &t);
+  count_scalars(L, f->vec, &f->rows);
+  count_scalars(L, f->vec, &f->narrow);
   // clusters: few tiles, none with more groups than a CTA's table of its cluster's sums holds
   f->cluster_ok = f->narrow.n() > 0 && f->narrow.n() <= GN_LOCAL_TILES && f->narrow.groups <= 32;
 }
