@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cstdint>
+#include <string>
 #include <vector>
 
 #include "../../include/e3b.h"
@@ -16,6 +17,13 @@ namespace e3b {
 constexpr int FR_MAXB = 32;             // irrep blocks at most
 constexpr int FR_MAX_L = 127;           // degree of a block at most
 constexpr int64_t FR_MAX_DIM = 32768;   // columns of a row at most
+
+// One term of an irreps string: multiplicity, degree, parity (+1 / -1).
+struct IrrepT {
+  int mul, l, p;
+};
+// Terms of an irreps string (host.cpp); false with the reason in *why when it is malformed.
+bool parse_irreps(const char* s, std::vector<IrrepT>* out, std::string* why);
 
 struct RowBlock {
   int32_t col0;        // first column

@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "cg_pattern.h"
+#include "features.h"
 #include "internal.h"
 
 namespace e3b {

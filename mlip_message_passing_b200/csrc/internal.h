@@ -40,13 +40,6 @@ namespace e3b {
 e3_status fail(e3_status st, const char* fmt, ...);
 void clear_error();
 
-// One term of an irreps string: multiplicity, degree, parity (+1 / -1).
-struct IrrepT {
-  int mul, l, p;
-};
-// Terms of an irreps string (host.cpp); false with the reason in *why when it is malformed.
-bool parse_irreps(const char* s, std::vector<IrrepT>* out, std::string* why);
-
 // Real-basis CG (ladder construction), dense [2l1+1][2l2+1][2l3+1], row-major.
 std::vector<double> real_cg_ladder(int l1, int l2, int l3);
 
