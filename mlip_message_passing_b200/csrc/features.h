@@ -7,7 +7,7 @@
 
 #include "../../include/e3b.h"
 
-#ifndef __CUDACC__
+#if !defined(__CUDACC__) && !defined(__host__)
 #define __host__
 #define __device__
 #endif
