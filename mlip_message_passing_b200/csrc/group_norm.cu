@@ -122,8 +122,7 @@ GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows,
     const int k = GN_THREADS / n->tx;
     int cs = 1;
     while (cs < 16 && int64_t(RP) * k * cs < most) cs *= 2;
-    // all clusters at once; in the backwards the clusters of a tile meet for the parameters' gradients, so
-    // there they have to be resident (counted as one CTA per SM), unless there is one per tile
+    // all clusters at once; in the backwards one CTA per SM, unless there is one cluster per tile
     const int64_t all = B * n->n();
     const int64_t room = op == GN_FWD || B == 1 ? 2 * sm_count() : 128;
     const bool fits = int64_t(RP) * k * cs >= most && all * cs <= room;
@@ -269,8 +268,11 @@ size_t gn_grid_layout(NormArgs* a, int op, int64_t ctas) {
   return tickets + al256(size_t(a->n_tiles) * 4);
 }
 
-size_t gn_local_layout(const NormArgs& a, int op, int vec, int64_t ctas) {
+size_t gn_column_bytes(const NormArgs& a, int op, int vec, int64_t ctas) {
   return op == GN_FWD ? 0 : al256(size_t(ctas) * 2 * size_t(a.tx) * size_t(vec) * 8);
+}
+size_t gn_local_layout(const NormArgs& a, int op, int vec, int64_t ctas) {
+  return gn_column_bytes(a, op, vec, ctas) + (op != GN_FWD && a.cs > 1 ? al256(size_t(a.n_tiles) * 4) : 0);
 }
 
 // Even scalars with the activation take a batch half as long again (three quarters in the double backward);

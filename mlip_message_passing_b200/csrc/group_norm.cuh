@@ -80,13 +80,13 @@ struct NormArgs {
   int32_t chunks;           // grid: row chunks
   int64_t rows_cta;         // grid: rows of a chunk
   int32_t parts;            // grid: parts of a chunk in the second pass
-  int32_t* tickets;         // grid: next part of each tile
+  int32_t* tickets;         // by tile.  grid: its next part; clusters: CTAs that have left their column sums (0 before)
   DropArgs drop;
   RowLayout lay;
   int32_t tile[GN_MAXTILE + 1];  // first vector column of each tile
   int32_t start[GN_LOCAL_TILES + 1];  // local: first CTA of each tile
   int32_t even;                       // local: all tiles have the same number of CTAs (blockIdx.y: the tile)
-  int32_t meet;                       // local: the grid meets for the parameters' gradients
+  int32_t meet;                       // local: the parameters' gradients add up more CTAs than one cluster
 };
 
 // Rows [s, e) of segment b, clamped into [0, N); a bad row pointer is recorded.
@@ -454,13 +454,13 @@ __device__ __forceinline__ void gn_store_columns(const double* colacc, double* o
 }
 
 // Gradients of the weights and biases of a tile's channels from the column sums of its `parts` CTAs (2 `apart`
-// between CTAs), after they have met; CTA `rank` takes its share.  A tile holds whole channels.
+// between CTAs), once all have left them; CTA `rank` of the `of` that call it takes its share.
 template <typename T, int VEC, int NT = GN_THREADS>
 __device__ __forceinline__ void gn_finish_columns(const NormArgs& a, const double* sums, int64_t apart, int parts,
-                                                  int v0, int W, int rank) {
+                                                  int v0, int W, int rank, int of) {
   constexpr int WARPS = NT / 32;
   const int lane = int(threadIdx.x) % 32, n = W * VEC;
-  for (int q = rank * WARPS + int(threadIdx.x) / 32; q < n; q += parts * WARPS) {
+  for (int q = rank * WARPS + int(threadIdx.x) / 32; q < n; q += of * WARPS) {
     const int col = v0 * VEC + q;
     const RowBlock& b = a.lay.blk[block_of(a.lay, col)];
     const int u = int(fast_div(uint32_t(col - b.col0), b.div_d));
@@ -481,6 +481,19 @@ __device__ __forceinline__ void gn_finish_columns(const NormArgs& a, const doubl
       if (bias) static_cast<T*>(a.gb)[b.bias0 + u] = T(sb);
     }
   }
+}
+
+// Is this CTA the last of `ctas` to come here?  What each stored before is then visible to it; nothing waits.
+// The counter starts at 0.  All threads call it; `flag` is an int of shared memory that no one else uses.
+__device__ __forceinline__ bool gn_comes_last(int32_t* counter, int ctas, int* flag) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    *flag = atomicAdd(counter, 1) == ctas - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  return *flag != 0;
 }
 
 // Local groups of a tile: their vector ranges.
@@ -922,9 +935,15 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
     const int apart = a.tx * VEC;
     double* sums = a.colpart + 2 * int64_t(a.start[tile]) * apart;
     gn_store_columns<VEC, NT>(colbase, sums + 2 * int64_t(at) * apart, apart, W, a.tx, J * K);
-    if (CL && !a.meet) cooperative_groups::this_cluster().sync();  // every tile has one cluster
+    if (CL && a.meet) {
+      // Clusters never meet across the grid: no launch has both a cluster dimension and a grid barrier.  The CTA
+      // of the tile that comes last adds up the sums of all, in the order of their numbers whichever it is.
+      if (gn_comes_last(a.tickets + tile, ctas, lens)) gn_finish_columns<T, VEC, NT>(a, sums, apart, ctas, v0, W, 0, 1);
+      return;
+    }
+    if (CL) cooperative_groups::this_cluster().sync();  // one cluster has all of the tile's segments
     else cooperative_groups::this_grid().sync();
-    gn_finish_columns<T, VEC, NT>(a, sums, apart, ctas, v0, W, at);
+    gn_finish_columns<T, VEC, NT>(a, sums, apart, ctas, v0, W, at, ctas);
   }
 }
 
@@ -1278,7 +1297,7 @@ __global__ void __launch_bounds__(GN_THREADS, OP == GN_FWD ? 3 : 2) gn_grid_kern
   bounds();
   p.b = first;
   there = lo < hi && open(true);  // the first rows are on their way while the grid meets
-  if (OP == GN_BWD && col_sums) gn_finish_columns<T, VEC>(a, csum, a.lay.dim, a.chunks, v0, W, rc);
+  if (OP == GN_BWD && col_sums) gn_finish_columns<T, VEC>(a, csum, a.lay.dim, a.chunks, v0, W, rc, a.chunks);
   grid.sync();
 
   while (true) {
@@ -1311,7 +1330,7 @@ __global__ void __launch_bounds__(GN_THREADS, OP == GN_FWD ? 3 : 2) gn_grid_kern
   if (OP == GN_DBL && col_sums) {
     gn_store_columns<VEC>(columns, csum + 2 * rc * int64_t(a.lay.dim), a.lay.dim, W, a.tx, K);
     grid.sync();
-    gn_finish_columns<T, VEC>(a, csum, a.lay.dim, a.chunks, v0, W, rc);
+    gn_finish_columns<T, VEC>(a, csum, a.lay.dim, a.chunks, v0, W, rc, a.chunks);
   }
 }
 

@@ -30,6 +30,8 @@ __host__ __device__ constexpr int gn_reg_segments(int op, int vec) {
 
 // Chunks and workspace of the grid kernel on `ctas` resident CTAs; returns the bytes needed.
 size_t gn_grid_layout(NormArgs* a, int op, int64_t ctas);
+// Workspace of the local kernel on `ctas` CTAs: their column sums, then (clusters) a counter by tile.
+size_t gn_column_bytes(const NormArgs& a, int op, int vec, int64_t ctas);
 size_t gn_local_layout(const NormArgs& a, int op, int vec, int64_t ctas);
 // Shares out `room` resident CTAs (clusters) among the tiles of the local kernel, `batches` of segments each.
 void gn_share(NormArgs* a, int op, const TileSet& t, int64_t batches, int64_t room);
@@ -118,7 +120,7 @@ e3_status gn_run_local(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s)
       if (dev < 64) clusters[dev][size].store(int64_t(smem) << 32 | n, std::memory_order_relaxed);
     }
     room = std::min<int64_t>(room, n);
-    // nothing waits for other clusters in the forward, nor where one cluster has all of a tile's segments
+    // no cluster waits for another
     if (n > 0) room = std::max<int64_t>(room, a.n_tiles);
   }
   if (room < a.n_tiles) return fail(E3_ERR_CUDA, "group norm: no room for the kernel on this device");
@@ -129,8 +131,13 @@ e3_status gn_run_local(NormArgs& a, const GnConfig& c, void* ws, cudaStream_t s)
   const bool columns = OP != GN_FWD && (a.gw != nullptr || a.gb != nullptr);
   a.colpart = columns ? static_cast<double*>(ws) : nullptr;
   a.meet = columns && !(CL && ctas == int64_t(a.n_tiles) * a.cs);
+  if (CL && a.meet) {
+    a.tickets = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + gn_column_bytes(a, OP, VEC, ctas));
+    if (cudaMemsetAsync(a.tickets, 0, sizeof(int32_t) * size_t(a.n_tiles), s) != cudaSuccess)
+      return fail(E3_ERR_CUDA, "group norm: zeroing the counters failed");
+  }
   const dim3 grid = a.even ? dim3(unsigned(a.start[1]), unsigned(a.n_tiles)) : dim3(unsigned(ctas));
-  return gn_start(kernel, a, grid, smem, a.meet != 0, a.cs, s, NT);
+  return gn_start(kernel, a, grid, smem, !CL && a.meet, a.cs, s, NT);
 }
 
 template <typename T, int VEC, int OP, bool DROP>

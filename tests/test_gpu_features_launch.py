@@ -1,0 +1,115 @@
+"""Launch forms and rare calls of the feature-row operators: what a captured call launches, sums of many rows,
+extreme values, parameters anywhere in memory, rows beyond 32-bit offsets in every kernel.
+
+Tolerances are in half steps of the type (2^-24 for float32) times the sum of the absolute values of the terms
+that make up an output, unless a test derives its own."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def e3b():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from mlip_message_passing_b200 import e3b
+    return e3b
+
+
+def _kernel_nodes(graph):
+    """(cooperative, CTAs of a cluster) of every kernel node of a captured graph, by the driver's graph calls."""
+    cu = ctypes.CDLL("libcuda.so.1")
+    handle = ctypes.c_void_p(graph.raw_cuda_graph())
+    n = ctypes.c_size_t()
+    assert cu.cuGraphGetNodes(handle, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert cu.cuGraphGetNodes(handle, nodes, ctypes.byref(n)) == 0
+    out = []
+    for node in nodes:
+        kind = ctypes.c_int()
+        assert cu.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        if kind.value != 0:  # a kernel
+            continue
+        value = {}
+        for attr in (2, 4):  # cooperative, cluster dimension
+            v = (ctypes.c_uint * 16)()
+            assert cu.cuGraphKernelNodeGetAttribute(ctypes.c_void_p(node), attr, v) == 0
+            value[attr] = list(v)
+        x, y, z = value[4][:3]
+        out.append((bool(value[2][0]), max(1, x) * max(1, y) * max(1, z)))
+    return out
+
+
+@pytest.mark.parametrize("irreps,groups,counts", [
+    ("32x0e+16x1o+8x2e", 4, [40, 0, 80]), ("16x0e+8x1o", 2, [300, 170]), ("64x0e+64x1o+64x2e", 8, [700])])
+def test_clusters_do_not_meet_across_the_grid(e3b, irreps, groups, counts):
+    """Segments held by clusters: the call is captured and not run, and no launch has both a cluster dimension
+    and the right to a grid barrier."""
+    f, seg = e3b.Features(irreps, groups=groups), e3b.Segments.from_counts(counts)
+    n = sum(counts)
+    x, g, u = (torch.zeros(n, f.dim, device=DEV) for _ in range(3))
+    stats = torch.zeros(len(counts), f.n_groups, 2, dtype=torch.float64, device=DEV)
+    e3b.group_norm_forward(f, x[:0].contiguous())  # sets the device's status word up
+    kw = dict(segments=seg, act="silu")
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        e3b.group_norm_forward(f, x, **kw)
+        e3b.group_norm_backward(f, x, stats, g, **kw)
+        e3b.group_norm_double_backward(f, x, stats, g, u_x=u, **kw)
+    nodes = _kernel_nodes(graph)
+    assert len(nodes) == 3 and sum(cluster > 1 for _, cluster in nodes) >= 2, nodes
+    assert not any(coop and cluster > 1 for coop, cluster in nodes), nodes
+    del graph
+
+
+def test_clusters_share_a_tile(e3b):
+    """Several clusters to a tile leave their column sums and the last to come adds them: the same bits in every
+    run, on two streams at once and in a replayed graph, and the oracle's values."""
+    irreps, groups, counts = "16x0e+8x1o", 2, [300, 0, 170, 450]
+    f, seg = e3b.Features(irreps, groups=groups), e3b.Segments.from_counts(counts)
+    n = sum(counts)
+    rng = np.random.default_rng(2)
+    xn, gn, un = (rng.standard_normal((n, f.dim)).astype(np.float32) for _ in range(3))
+    x, g, u = (torch.as_tensor(t, device=DEV) for t in (xn, gn, un))
+    kw = dict(segments=seg, act="silu", p=0.2, rng=(6, 1))
+
+    def run():
+        _, st = e3b.group_norm_forward(f, x, **kw)
+        return (*e3b.group_norm_backward(f, x, st, g, **kw), *e3b.group_norm_double_backward(f, x, st, g, u_x=u, **kw))
+
+    want = run()
+    okw = dict(act="silu", factor=oracle.dropout_factor(irreps, n, 0.2, 6, 1), scale=True)
+    ptr = np.concatenate([[0], np.cumsum(counts)])
+    first = oracle.group_norm_backward(irreps, groups, ptr, xn, gn, **okw)
+    second = oracle.group_norm_double_backward(irreps, groups, ptr, xn, gn, u_x=un, **okw)
+    # 96 and 288: a thread's float sums of at most 64 rows (of four columns) and at most 32 pointwise roundings
+    for got, ref, size, steps in (*((want[i], first[i], first[i + 3], 96) for i in range(3)),
+                                  *((want[i + 3], second[i], second[i + 4], 288) for i in range(4))):
+        assert (np.abs(got.cpu().double().numpy() - ref) <= steps * 2.0 ** -24 * size + 1e-30).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = run()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        res = []
+        for s in side:
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                res.append(run())
+        for s in side:
+            torch.cuda.current_stream().wait_stream(s)
+        graph.replay()
+        res.append(kept)
+        torch.cuda.synchronize()
+        for r in res:
+            assert all(torch.equal(a, b) for a, b in zip(r, want))
+    e3b.device_status()
+    del graph
