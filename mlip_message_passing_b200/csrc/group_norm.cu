@@ -28,16 +28,20 @@ void count_scalars(const RowLayout& L, int vec, TileSet* t) {
   }
 }
 
-// Tiles of whole groups, as many as fit `cap` vectors (cap >= the widest group).
-TileSet cut_tiles(const RowLayout& L, int vec, int cap) {
+// Tiles of whole groups, as many as fit `cap` vectors (cap >= the widest group), `most` at most.
+TileSet cut_tiles(const RowLayout& L, int vec, int cap, int most = 1 << 30) {
   TileSet t;
   t.first.push_back(0);
-  int at = 0;
+  int at = 0, held = 0;
   for (int b = 0; b < L.n_blocks; ++b) {
     const int w = L.blk[b].group_cols / vec;
     for (int g = 0; g < L.groups; ++g) {
-      if (at + w - t.first.back() > cap && at > t.first.back()) t.first.push_back(at);
+      if (held > 0 && (at + w - t.first.back() > cap || held == most)) {
+        t.first.push_back(at);
+        held = 0;
+      }
       at += w;
+      ++held;
     }
   }
   t.first.push_back(at);
@@ -68,12 +72,12 @@ TileSet equal_tiles(const RowLayout& L, int vec) {
 
 // The cut between `lo` and `hi` that leaves the fewest of a block's threads idle; of cuts within 3% of it the
 // widest, whose rows are the longest runs of memory.
-TileSet best_tiles(const RowLayout& L, int vec, int lo, int hi, int k, int threads) {
+TileSet best_tiles(const RowLayout& L, int vec, int lo, int hi, int k, int threads, int most = 1 << 30) {
   TileSet best;
   double score = -1.0;
   const int V = L.dim / vec;
   for (int cap = lo; cap <= hi; ++cap) {
-    TileSet t = cut_tiles(L, vec, cap);
+    TileSet t = cut_tiles(L, vec, cap, most);
     if (t.n() > GN_MAXTILE) continue;
     const int lanes = k > 0 ? k * std::max(1, threads / (t.tx * k)) : threads / t.tx;
     const double u = double(V) / (double(t.n()) * t.tx) * (double(t.tx) * lanes / threads);
@@ -107,8 +111,7 @@ GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows,
     c.local = c.one_row = true;
     t = &f->rows;
     a->cap = a->k = 1;
-    // the items' coefficients stay below 2048
-    a->j = std::min(GN_ROW_THREADS / t->tx, std::max(1, 2048 / (gn_reg_segments(op, f->vec) * t->groups)));
+    a->j = std::min(GN_ROW_THREADS / t->tx, GN_ROW_ITEMS / (gn_reg_segments(op, f->vec) * t->groups));
   } else if (t->n() > 0 && t->n() <= GN_LOCAL_TILES && (held || turns)) {
     c.local = true;
     a->cap = held ? RP : GN_FLUSH;
@@ -235,7 +238,9 @@ void make_tiles(e3_features* f) {
   for (int i = 0; i < 9; ++i)
     if ((f->wide << i) <= GN_THREADS)
       f->local[i] = best_tiles(L, f->vec, f->wide, GN_THREADS >> i, 1 << i, GN_THREADS);
-  if (f->wide <= GN_ROW_THREADS) f->rows = best_tiles(L, f->vec, f->wide, GN_ROW_THREADS, 1, GN_ROW_THREADS);
+  if (f->wide <= GN_ROW_THREADS)
+    f->rows = best_tiles(L, f->vec, f->wide, GN_ROW_THREADS, 1, GN_ROW_THREADS,
+                         GN_ROW_ITEMS / gn_reg_segments(GN_FWD, f->vec));
   f->grid = equal_tiles(L, f->vec);
   // narrow tiles for clusters, which leave the CTAs more row lanes
   if (f->wide <= 64) f->narrow = cut_tiles(L, f->vec, std::max(f->wide, 8));

@@ -11,6 +11,7 @@ import pytest
 import torch
 
 import oracle
+from test_gpu_features import _check_all
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -113,3 +114,11 @@ def test_clusters_share_a_tile(e3b):
             assert all(torch.equal(a, b) for a, b in zip(r, want))
     e3b.device_status()
     del graph
+
+
+@pytest.mark.parametrize("irreps,groups", [("512x0e", 512), ("256x0e+256x0o", 256), ("1024x0e", 1024),
+                                           ("+".join(["16x0o"] * 32), 16), ("+".join(["100x0e"] * 5), 100)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float64])
+def test_one_row_segments_of_many_groups(e3b, irreps, groups, dtype):
+    """Hundreds of one-column groups to a tile: the coefficients of a batch have to fit shared memory."""
+    _check_all(e3b, irreps, groups, [1] * 20, 3, dtype, "silu", 0.1, seed=6)
