@@ -833,6 +833,7 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
   const uint32_t div_j = J > 1 ? 0xFFFFFFFFu / uint32_t(J) + 1u : 0u;
   const int lane = tid & (a.lanes - 1), sub = tid / a.lanes, per = NT / a.lanes;
   const int items = M * J * nlg;
+  const int held = M * (TURNS ? a.cap : R);  // rows of a thread in a batch at most
   int rows_held = 0, parity = 0;
   if (CL) cooperative_groups::this_cluster().sync();  // every CTA of the cluster has started
   for (; b0 < a.B; b0 += hop_b, parity ^= 1) {
@@ -911,8 +912,8 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
     else if (c.kind == GN_CENTRED)
       gn_local_apply<GN_CENTRED, TURNS, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, t, step, q, hop_res, cw, cb);
     else gn_local_apply<GN_ACT, TURNS, T, VEC, OP, DROP, R, M, NT>(a, c, st, sl, t, step, q, hop_res, cw, cb);
-    rows_held += R * M;
-    if (columns && rows_held >= GN_FLUSH) {
+    rows_held += held;
+    if (columns && rows_held > GN_FLUSH - held) {  // another batch could pass GN_FLUSH rows
       rows_held = 0;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {

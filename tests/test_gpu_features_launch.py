@@ -122,3 +122,24 @@ def test_clusters_share_a_tile(e3b):
 def test_one_row_segments_of_many_groups(e3b, irreps, groups, dtype):
     """Hundreds of one-column groups to a tile: the coefficients of a batch have to fit shared memory."""
     _check_all(e3b, irreps, groups, [1] * 20, 3, dtype, "silu", 0.1, seed=6)
+
+
+def test_parameter_gradients_of_segments_that_take_turns(e3b):
+    """5032 segments of 64 rows, whose rows take a thread's slots in turns: the weight gradients of a column are sums of
+    N equal terms t = 1 + 2^-16 (1 - 2^-6).  A float32 sum of them drops 2^-16 of every term once it is above 256, so a
+    thread that went on for more than 64 rows before its sums go to double would be off by up to 180 half steps.
+    With 64 rows it is off by 64 half steps at most, and by 32 for the pointwise part."""
+    irreps, B = "85x1o", 5032
+    f, seg = e3b.Features(irreps), e3b.Segments.from_counts([64] * B)
+    n, t = 64 * B, 1 + 2.0 ** -16 * (1 - 2.0 ** -6)
+    one = torch.ones(n, f.dim, device=DEV)
+    x = one.clone()
+    x[1::2] = -1  # sums of z u vanish, z = x: the mean square is 1
+    kw = dict(segments=seg, act=None)
+    _, stats = e3b.group_norm_forward(f, x, eps=1e-30, segments=seg)
+    bound = (64 + 32) * 2.0 ** -24 * n * 3 * t  # a channel has three columns
+    _, gw, _ = e3b.group_norm_backward(f, x, stats, x * t, need_x=False, **kw)
+    assert float((gw.double() - n * 3 * t).abs().max()) <= bound
+    _, _, dw, _ = e3b.group_norm_double_backward(f, x, stats, one * t, u_x=one, **kw)
+    assert float((dw.double() - n * 3 * t).abs().max()) <= bound
+    e3b.device_status()
