@@ -344,7 +344,10 @@ extern "C" e3_status e3_group_norm_forward(const e3_features* f, int64_t N, int6
   clear_error();
   e3_status st = check_sizes(f, N, B, row_ptr != nullptr);
   if (st != E3_OK) return st;
-  if (!(eps > 0.0) || !std::isfinite(eps)) return fail(E3_ERR_INVALID_ARG, "eps = %g must be positive", eps);
+  // the kernels add eps in the rows' type
+  const double added = f->dtype == E3_F32 ? double(float(eps)) : eps;
+  if (!(added > 0.0) || !std::isfinite(added))
+    return fail(E3_ERR_INVALID_ARG, "eps = %g must be positive and finite in the rows' type", eps);
   NormArgs a{};
   GnConfig c;
   bool on = false;

@@ -143,3 +143,19 @@ def test_parameter_gradients_of_segments_that_take_turns(e3b):
     _, _, dw, _ = e3b.group_norm_double_backward(f, x, stats, one * t, u_x=one, **kw)
     assert float((dw.double() - n * 3 * t).abs().max()) <= bound
     e3b.device_status()
+
+
+def test_eps_that_vanishes_in_the_rows_type_is_refused(e3b):
+    """1e-50 is 0 as a float32 and 1e39 infinite: a constant group would become NaN.  float64 rows take both."""
+    for dtype in (torch.float32, torch.float64):
+        f = e3b.Features("8x0e+8x1o", groups=2, dtype=dtype)
+        x = torch.zeros(10, 32, device=DEV, dtype=dtype)
+        for eps in (1e-50, 1e39):
+            if dtype is torch.float32:
+                with pytest.raises(e3b.E3Error) as err:
+                    e3b.group_norm_forward(f, x, eps=eps)
+                assert err.value.status == e3b.E3_ERR_INVALID_ARG
+            else:
+                assert not bool(e3b.group_norm_forward(f, x, eps=eps)[0].any())
+        y, _ = e3b.group_norm_forward(f, x, eps=1e-44)  # a subnormal float32 number
+        assert not bool(y.any())
