@@ -345,7 +345,8 @@ struct GnAcc<T, VEC, GN_DBL, DROP> {
 
 __device__ __forceinline__ float gn_rsqrt(float v) {
   const float r = rsqrtf(v);
-  return fmaf(0.5f * r, fmaf(-v * r, r, 1.f), r);  // one Newton step: the hardware's result is 2 ulp off
+  const float n = fmaf(0.5f * r, fmaf(-v * r, r, 1.f), r);  // one Newton step: the hardware's result is 2 ulp off
+  return r > 0.f ? n : r;                                   // 0 for an infinite v, where the step is inf * 0
 }
 __device__ __forceinline__ double gn_rsqrt(double v) { return 1.0 / sqrt(v); }
 __device__ __forceinline__ float gn_recip(float v) { return __fdividef(1.f, v); }

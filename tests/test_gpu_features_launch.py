@@ -159,3 +159,36 @@ def test_eps_that_vanishes_in_the_rows_type_is_refused(e3b):
                 assert not bool(e3b.group_norm_forward(f, x, eps=eps)[0].any())
         y, _ = e3b.group_norm_forward(f, x, eps=1e-44)  # a subnormal float32 number
         assert not bool(y.any())
+
+
+@pytest.mark.parametrize("counts,hint", [([10, 10, 10], "max"), ([10, 10, 10], 0), ([1] * 30, "max"), ([30], "max")])
+def test_infinite_mean_square_gives_zero(e3b, counts, hint):
+    """A value whose square no float32 holds: r = 1 / sqrt(inf) = 0, so its group is t = bias, not NaN, and takes no
+    part in the gradients; the other groups are what they are without it."""
+    f, seg = e3b.Features("8x0e+8x1o", groups=2), e3b.Segments.from_counts(counts)
+    if hint != "max":
+        seg.max_rows = hint
+    gen = torch.Generator(DEV).manual_seed(1)
+    x, g, u = (torch.randn(30, 32, device=DEV, generator=gen) for _ in range(3))
+    b = torch.randn(8, device=DEV, generator=gen)
+    big = x.clone()
+    big[4, 1] = 1e25    # scalars, first group
+    big[4, 20] = -1e25  # vectors, second group
+    first = next(i for i, e in enumerate(np.cumsum(counts)) if e > 4)
+    lo, hi = sum(counts[:first]), sum(counts[:first + 1])
+    bad = torch.zeros(30, 32, dtype=torch.bool, device=DEV)
+    bad[lo:hi, :4] = True
+    bad[lo:hi, 20:] = True
+    out = []
+    for src in (x, big):
+        y, st = e3b.group_norm_forward(f, src, None, b, segments=seg)
+        gx = e3b.group_norm_backward(f, src, st, g, None, b, segments=seg)[0]
+        dg, dx, _, _ = e3b.group_norm_double_backward(f, src, st, g, None, b, u_x=u, segments=seg)
+        out.append((y, gx, dg, dx))
+    for a, c in zip(*out):
+        assert torch.equal(a[~bad], c[~bad])
+    y, gx, dg, dx = out[1]
+    assert torch.equal(y[lo:hi, :4], b[:4].expand(hi - lo, 4)) and not bool(y[lo:hi, 20:].any())
+    for t in (gx, dg, dx):
+        assert not bool(t[bad].any())
+    e3b.device_status()
