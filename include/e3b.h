@@ -383,7 +383,8 @@ typedef enum { E3_ACT_NONE = 0, E3_ACT_SILU = 1 } e3_act;
  *            rows touched stay inside [0, N); results are then unspecified).
  *   max_rows an upper bound on the rows of a segment, or 0 if unknown; it selects the kernels.  A segment
  *            that is longer records E3_ERR_INDEX where its surplus rows find no place (they are skipped).
- *   weight   [n_channels] or NULL (ones); bias [n_scalars] or NULL (zeros);
+ *   weight   [n_channels] or NULL (ones); bias [n_scalars] or NULL (zeros): element-aligned, as their
+ *            gradients are in the calls below;
  *   eps      positive and finite, also when rounded to the rows' type (as is the sum of squares: float32
  *            values beyond 1e19 or so make it infinite, then r = 0 and z = 0 in that segment and group);
  *   drop     NULL: none;

@@ -186,8 +186,9 @@ e3_status check_sizes(const e3_features* f, int64_t N, int64_t B, bool one_ok) {
   return E3_OK;
 }
 
-e3_status check_pointers(const void* const* required, const char* const* names, int n, const void* const* optional,
-                         int m) {
+// Rows (and statistics) are moved in 16-byte vectors; `params` are read and written element by element.
+e3_status check_pointers(const e3_features* f, const void* const* required, const char* const* names, int n,
+                         const void* const* optional, int m, const void* const* params, int k) {
   for (int i = 0; i < n; ++i) {
     if (required[i] == nullptr) return fail(E3_ERR_INVALID_ARG, "%s is NULL", names[i]);
     if (reinterpret_cast<uintptr_t>(required[i]) & 15u)
@@ -196,6 +197,10 @@ e3_status check_pointers(const void* const* required, const char* const* names, 
   for (int i = 0; i < m; ++i)
     if (reinterpret_cast<uintptr_t>(optional[i]) & 15u)
       return fail(E3_ERR_INVALID_ARG, "an optional pointer is not 16-byte aligned");
+  const uintptr_t element = f->dtype == E3_F64 ? 8 : 4;
+  for (int i = 0; i < k; ++i)
+    if (reinterpret_cast<uintptr_t>(params[i]) & (element - 1))
+      return fail(E3_ERR_INVALID_ARG, "a weight, a bias or its gradient is not aligned to its type");
   return E3_OK;
 }
 
@@ -355,8 +360,8 @@ extern "C" e3_status e3_group_norm_forward(const e3_features* f, int64_t N, int6
   if (st != E3_OK || N == 0) return st;
   const void* req[3] = {x, y, stats};
   const char* names[3] = {"x", "y", "stats"};
-  const void* opt[2] = {weight, bias};
-  if ((st = check_pointers(req, names, 3, opt, 2)) != E3_OK) return st;
+  const void* params[2] = {weight, bias};
+  if ((st = check_pointers(f, req, names, 3, nullptr, 0, params, 2)) != E3_OK) return st;
   a.x = x;
   a.w = weight;
   a.b = bias;
@@ -383,8 +388,9 @@ extern "C" e3_status e3_group_norm_backward(const e3_features* f, int64_t N, int
   if (N == 0) return zero_params(f, grad_weight, grad_bias, s);
   const void* req[3] = {x, stats, grad_y};
   const char* names[3] = {"x", "stats", "grad_y"};
-  const void* opt[5] = {weight, bias, grad_x, grad_weight, grad_bias};
-  if ((st = check_pointers(req, names, 3, opt, 5)) != E3_OK) return st;
+  const void* opt[1] = {grad_x};
+  const void* params[4] = {weight, bias, grad_weight, grad_bias};
+  if ((st = check_pointers(f, req, names, 3, opt, 1, params, 4)) != E3_OK) return st;
   a.x = x;
   a.g = grad_y;
   a.w = weight;
@@ -416,8 +422,9 @@ extern "C" e3_status e3_group_norm_double_backward(const e3_features* f, int64_t
   if (N == 0) return zero_params(f, d_weight, d_bias, s);
   const void* req[3] = {x, stats, grad_y};
   const char* names[3] = {"x", "stats", "grad_y"};
-  const void* opt[9] = {weight, bias, u_x, u_weight, u_bias, d_grad_y, d_x, d_weight, d_bias};
-  if ((st = check_pointers(req, names, 3, opt, 9)) != E3_OK) return st;
+  const void* opt[3] = {u_x, d_grad_y, d_x};
+  const void* params[6] = {weight, bias, u_weight, u_bias, d_weight, d_bias};
+  if ((st = check_pointers(f, req, names, 3, opt, 3, params, 6)) != E3_OK) return st;
   a.x = x;
   a.g = grad_y;
   a.u = u_x;

@@ -192,3 +192,29 @@ def test_infinite_mean_square_gives_zero(e3b, counts, hint):
     for t in (gx, dg, dx):
         assert not bool(t[bad].any())
     e3b.device_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float64])
+def test_parameters_anywhere_in_a_flat_buffer(e3b, dtype):
+    """Weights, biases and their upstream gradients are slices of one buffer that start off every vector boundary."""
+    f, seg = e3b.Features("5x0e+3x1o", dtype=dtype), e3b.Segments.from_counts([4, 0, 9])
+    gen = torch.Generator(DEV).manual_seed(1)
+    flat = torch.randn(60, device=DEV, dtype=dtype, generator=gen)
+    w, b, uw, ub = flat[1:9], flat[9:14], flat[23:31], flat[31:36]
+    x, g, u = (torch.randn(13, f.dim, device=DEV, dtype=dtype, generator=gen) for _ in range(3))
+
+    def run(w, b, uw, ub):
+        y, st = e3b.group_norm_forward(f, x, w, b, segments=seg, act="silu")
+        return (y, *e3b.group_norm_backward(f, x, st, g, w, b, segments=seg, act="silu"),
+                *e3b.group_norm_double_backward(f, x, st, g, w, b, u, uw, ub, segments=seg, act="silu"))
+
+    for got, want in zip(run(w, b, uw, ub), run(*(t.clone() for t in (w, b, uw, ub)))):
+        assert torch.equal(got, want)
+    leaf = flat.clone().requires_grad_(True)
+    y = e3b.group_norm(f, x, leaf[1:9], leaf[9:14], segments=seg, act="silu")
+    (grad,) = torch.autograd.grad(y, leaf, g)
+    _, st = e3b.group_norm_forward(f, x, w, b, segments=seg, act="silu")
+    _, gw, gb = e3b.group_norm_backward(f, x, st, g, w, b, segments=seg, act="silu")
+    want = torch.zeros_like(flat)
+    want[1:9], want[9:14] = gw, gb
+    assert torch.equal(grad, want)
