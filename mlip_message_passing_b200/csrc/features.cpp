@@ -92,7 +92,7 @@ e3_status e3b::drop_args(const e3_dropout_spec* drop, int64_t N, DropArgs* out, 
   *on = false;
   if (drop == nullptr) return E3_OK;
   if (!(drop->p >= 0.0 && drop->p < 1.0)) return fail(E3_ERR_INVALID_ARG, "dropout p = %g is not in [0, 1)", drop->p);
-  if (drop->row0 < 0 || drop->row0 + N > (int64_t(1) << 32))
+  if (drop->row0 < 0 || drop->row0 > (int64_t(1) << 32) - N)
     return fail(E3_ERR_SHAPE, "dropout rows %lld .. + %lld pass 2^32", (long long)drop->row0, (long long)N);
   if (drop->state == nullptr && drop->offset >= (uint64_t(1) << 32))
     return fail(E3_ERR_INVALID_ARG, "dropout offset passes 2^32");

@@ -770,6 +770,8 @@ def _drop_spec(features, p, rng, row0):
         raise ValueError(f"p must be in [0, 1), got {p}")
     if rng is None:
         raise ValueError("dropout needs rng: a seed, a (seed, offset) pair or an int64 CUDA tensor [2]")
+    if not -2 ** 63 <= int(row0) < 2 ** 63:
+        raise ValueError("row0 must fit 64 bits")
     if isinstance(rng, torch.Tensor):
         _need(rng, "rng", torch.int64, (2,), features.device)
         return ctypes.byref(DropoutSpec(p, 0, 0, rng.data_ptr(), int(row0)))

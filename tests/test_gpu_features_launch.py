@@ -218,3 +218,19 @@ def test_parameters_anywhere_in_a_flat_buffer(e3b, dtype):
     want = torch.zeros_like(flat)
     want[1:9], want[9:14] = gw, gb
     assert torch.equal(grad, want)
+
+
+def test_first_row_beyond_32_bits_is_refused(e3b):
+    """row0 near 2^63 (where row0 + N overflows) and past 64 bits: not a mask of another row."""
+    f = e3b.Features("8x0e")
+    x = torch.ones(10, 8, device=DEV)
+    for call in (lambda r: e3b.dropout_forward(f, x, 0.5, 1, row0=r),
+                 lambda r: e3b.group_norm_forward(f, x, p=0.5, rng=1, row0=r)):
+        for row0 in (2 ** 63 - 1, 2 ** 63 - 10, 2 ** 32 - 9, 2 ** 32, -1, -2 ** 63):
+            with pytest.raises(e3b.E3Error) as err:
+                call(row0)
+            assert err.value.status == e3b.E3_ERR_SHAPE
+        for row0 in (2 ** 63, 2 ** 64, 2 ** 64 + 5, -2 ** 63 - 1):
+            with pytest.raises(ValueError):
+                call(row0)
+        call(2 ** 32 - 10)
