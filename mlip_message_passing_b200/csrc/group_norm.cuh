@@ -796,7 +796,7 @@ gn_local_kernel(const __grid_constant__ NormArgs a) {
       if (s < 0 || e < s || e > int(a.N) || e - s > a.cap * step) {  // no row pointer, or longer than the caller said
         atomicCAS(a.status, 0, int(E3_ERR_INDEX));
         s = min(max(s, 0), int(a.N));
-        e = min(min(max(e, s), int(a.N)), s + a.cap * step);
+        e = s + min(min(max(e, s), int(a.N)) - s, a.cap * step);
       }
       t.row0[m] = s + k;
       const int left = e - s - k + step - 1;

@@ -234,3 +234,18 @@ def test_first_row_beyond_32_bits_is_refused(e3b):
             with pytest.raises(ValueError):
                 call(row0)
         call(2 ** 32 - 10)
+
+
+def test_bad_row_pointers_of_the_longest_arrays(e3b):
+    """N = 2^31 - 65536 rows and pointers beyond them: a segment's clamped end stays inside [0, N], though start plus
+    the rows that a cluster holds (65536) passes 2^31."""
+    f, n = e3b.Features("1x0e"), 2 ** 31 - 65536
+    x = torch.zeros(n, 1, device=DEV)
+    ptr = torch.tensor([0, 2 ** 31 - 1, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    y, _ = e3b.group_norm_forward(f, x, segments=e3b.Segments(ptr, n, max_rows=65536))
+    with pytest.raises(e3b.E3Error) as err:
+        e3b.device_status()
+    assert err.value.status == e3b.E3_ERR_INDEX
+    assert not bool(y[:65536].any())
+    del x, y
+    torch.cuda.empty_cache()
