@@ -920,12 +920,14 @@ class _NormFn(torch.autograd.Function):
         ctx.features, ctx.rng = features, rng
         ctx.kw = dict(segments=segments, act=act, p=p, row0=row0)
         y, stats = group_norm_forward(features, x, weight, bias, eps=eps, rng=rng, **ctx.kw)
-        ctx.save_for_backward(x, weight, bias, stats, rng if isinstance(rng, torch.Tensor) else None)
+        # the row pointer too: one that changes before the backward is refused, as a changed x is
+        ctx.save_for_backward(x, weight, bias, stats, rng if isinstance(rng, torch.Tensor) else None,
+                              None if segments is None else segments.row_ptr)
         return y
 
     @staticmethod
     def backward(ctx, g):
-        x, weight, bias, stats, rng = ctx.saved_tensors
+        x, weight, bias, stats, rng, _ = ctx.saved_tensors
         gx, gw, gb = _NormBwdFn.apply(x, weight, bias, _operand(g), stats, ctx.features,
                                       ctx.rng if rng is None else rng, tuple(ctx.needs_input_grad[:3]), ctx.kw)
         return gx, gw, gb, None, None, None, None, None, None, None
@@ -937,7 +939,8 @@ class _NormBwdFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, g, stats, features, rng, needs, kw):
         ctx.features, ctx.rng, ctx.kw = features, rng, kw
-        ctx.save_for_backward(x, weight, bias, g, stats, rng if isinstance(rng, torch.Tensor) else None)
+        ctx.save_for_backward(x, weight, bias, g, stats, rng if isinstance(rng, torch.Tensor) else None,
+                              None if kw["segments"] is None else kw["segments"].row_ptr)
         ctx.set_materialize_grads(False)
         return group_norm_backward(features, x, stats, g, weight, bias, rng=rng, need_x=needs[0],
                                    need_weight=needs[1], need_bias=needs[2], **kw)
@@ -945,7 +948,7 @@ class _NormBwdFn(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, ux, uw, ub):
-        x, weight, bias, g, stats, rng = ctx.saved_tensors
+        x, weight, bias, g, stats, rng, _ = ctx.saved_tensors
         nx, nw, nb, ng = ctx.needs_input_grad[:4]
         dg, dx, dw, db = group_norm_double_backward(
             ctx.features, x, stats, g, weight, bias, u_x=_operand(ux), u_weight=_operand(uw),
@@ -956,5 +959,6 @@ class _NormBwdFn(torch.autograd.Function):
 
 def group_norm(features, x, weight=None, bias=None, segments=None, eps=1e-5, act=None, p=0.0, rng=None, row0=0):
     """Twice-differentiable group norm with activation and dropout (x, weight, bias; see
-    ``group_norm_forward``).  An rng tensor must keep its values until the backward has run."""
+    ``group_norm_forward``).  An rng tensor, and the segments' row pointer, must keep their values until the
+    backward has run."""
     return _NormFn.apply(x, weight, bias, features, segments, eps, act, p, rng, row0)

@@ -249,3 +249,22 @@ def test_bad_row_pointers_of_the_longest_arrays(e3b):
     assert not bool(y[:65536].any())
     del x, y
     torch.cuda.empty_cache()
+
+
+def test_row_pointer_that_changed_before_the_backward_is_refused(e3b):
+    """A row pointer in a buffer that the next batch overwrites: the gradient of the earlier batch would be taken over
+    other segments.  Both derivatives refuse it."""
+    f = e3b.Features("8x0e+4x1o", groups=2)
+    gen = torch.Generator(DEV).manual_seed(4)
+    x, g = (torch.randn(30, f.dim, device=DEV, generator=gen) for _ in range(2))
+    ptr = torch.tensor([0, 10, 30], dtype=torch.int32, device=DEV)
+    seg = e3b.Segments(ptr, 30, max_rows=20)
+    for second in (False, True):
+        leaf = x.clone().requires_grad_(True)
+        y = e3b.group_norm(f, leaf, segments=seg, act="silu")
+        if second:
+            (y,) = torch.autograd.grad(y, leaf, g, create_graph=True)
+        ptr[1] = 12
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(y, leaf, g)
+        ptr[1] = 10
