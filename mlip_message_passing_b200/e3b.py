@@ -819,7 +819,7 @@ class _DropoutFn(torch.autograd.Function):
 def dropout(features, x, p, rng, residual=None, row0=0):
     """Differentiable (any order) dropout of whole channels plus an optional residual; see
     ``dropout_forward``.  An rng tensor must keep its values until the backward has run."""
-    return _DropoutFn.apply(x, residual, features, p, rng, row0)
+    return _DropoutFn.apply(x, residual, features, p, tuple(rng) if isinstance(rng, list) else rng, row0)
 
 
 def _norm_args(features, x, weight, bias, segments, act):
@@ -961,4 +961,5 @@ def group_norm(features, x, weight=None, bias=None, segments=None, eps=1e-5, act
     """Twice-differentiable group norm with activation and dropout (x, weight, bias; see
     ``group_norm_forward``).  An rng tensor, and the segments' row pointer, must keep their values until the
     backward has run."""
+    rng = tuple(rng) if isinstance(rng, list) else rng  # a list could change before the backward
     return _NormFn.apply(x, weight, bias, features, segments, eps, act, p, rng, row0)

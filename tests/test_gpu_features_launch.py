@@ -268,3 +268,19 @@ def test_row_pointer_that_changed_before_the_backward_is_refused(e3b):
         with pytest.raises(RuntimeError):
             torch.autograd.grad(y, leaf, g)
         ptr[1] = 10
+
+
+def test_generator_list_that_counts_on(e3b):
+    """rng as a list [seed, offset] that the caller advances after the call: the backward drops what the forward did."""
+    f = e3b.Features("8x0e+4x1o", groups=2)
+    gen = torch.Generator(DEV).manual_seed(4)
+    x, g = (torch.randn(30, f.dim, device=DEV, generator=gen) for _ in range(2))
+    for op in (lambda t, rng: e3b.dropout(f, t, 0.5, rng), lambda t, rng: e3b.group_norm(f, t, p=0.5, rng=rng)):
+        grads = []
+        for rng in ([3, 0], (3, 0)):
+            leaf = x.clone().requires_grad_(True)
+            y = op(leaf, rng)
+            if isinstance(rng, list):
+                rng[1] += 1
+            grads.append(torch.autograd.grad(y, leaf, g)[0])
+        assert torch.equal(*grads)
