@@ -456,6 +456,8 @@ __device__ __forceinline__ void gn_store_columns(const double* colacc, double* o
 
 // Gradients of the weights and biases of a tile's channels from the column sums of its `parts` CTAs (2 `apart`
 // between CTAs), once all have left them; CTA `rank` of the `of` that call it takes its share.
+// All columns of a channel are read here: either a tile holds whole channels (local kernels), or `apart` is the
+// whole row and every tile's CTAs have left their sums (the grid kernel's tiles end anywhere, also in a channel).
 template <typename T, int VEC, int NT = GN_THREADS>
 __device__ __forceinline__ void gn_finish_columns(const NormArgs& a, const double* sums, int64_t apart, int parts,
                                                   int v0, int W, int rank, int of) {

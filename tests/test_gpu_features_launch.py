@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import oracle
-from test_gpu_features import _check_all
+from test_gpu_features import _check_all, _close
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -284,3 +284,117 @@ def test_generator_list_that_counts_on(e3b):
                 rng[1] += 1
             grads.append(torch.autograd.grad(y, leaf, g)[0])
         assert torch.equal(*grads)
+
+
+def test_tiles_that_end_inside_a_channel(e3b):
+    """Long segments of 2048 columns: two tiles of 1024, and column 1024 is one of channel 102 of the 2e block."""
+    _check_all(e3b, "128x0e+128x1o+128x2e+128x3o", 16, [300, 0, 40], 2, torch.float32, "silu", 0.0, seed=8, hint=0)
+
+
+def _gradient_sizes(irreps, groups, counts, t, act, factor):
+    """float64 weight and bias gradients of the norm's first and second derivative, and the size of each on which
+    rounding acts: the same sums with every term replaced by the sum of its parts' absolute values.  (The activation's
+    derivatives are products of the sigmoid, below 1, with 1 + t (1 - s) and 2 + t (1 - 2 s).)"""
+    seg = torch.repeat_interleave(torch.arange(len(counts), device=DEV), torch.tensor(counts, device=DEV))
+    n = torch.tensor(counts, device=DEV, dtype=torch.float64).clamp(min=1)
+    out, ch, sc = {k: [] for k in ("gw", "gb", "dw", "db", "gw_", "gb_", "dw_", "db_")}, 0, 0
+    col = 0
+    for ir in oracle.parse_irreps(irreps):
+        d, scalar = 2 * ir.l + 1, ir.l == 0 and ir.p == 1
+        take = lambda v: v[:, col:col + ir.mul * d].reshape(v.shape[0], groups, -1, d)
+        chan = lambda v, first: v[first:first + ir.mul].reshape(1, groups, -1, 1)
+
+        def mean(v):
+            s = torch.zeros(len(counts), groups, device=DEV, dtype=torch.float64)
+            s.index_add_(0, seg, v.sum(dim=(2, 3)))
+            return (s / (n * (ir.mul // groups * d))[:, None])[seg][:, :, None, None]
+
+        x, g, u, m = take(t["x"]), take(t["g"]), take(t["ux"]), take(factor)
+        w, uw = chan(t["w"], ch), chan(t["uw"], ch)
+        b, ub = (chan(t[k], sc) if scalar else torch.zeros(1, 1, 1, 1, device=DEV, dtype=torch.float64) for k in ("b", "ub"))
+        mu = mean(x) if scalar else 0 * mean(x)
+        r = torch.rsqrt(mean((x - mu) ** 2) + 1e-5)
+        z, za = (x - mu) * r, (x.abs() + mu.abs()) * r
+        tt, ta = w * z + b, w.abs() * za + b.abs()
+        on = scalar and act
+        s = torch.sigmoid(tt)
+        d1, d2 = (s * (1 + tt * (1 - s)), s * (1 - s) * (2 + tt * (1 - 2 * s))) if on else (1.0, 0.0)
+        h, ha = m * g * d1, m * g.abs() * ((1 + ta) if on else 1.0)
+        m1, m1a = (mean(u), mean(u.abs())) if scalar else (0.0, 0.0)
+        zd, zda = r * (u - m1 - z * mean(z * u)), r * (u.abs() + m1a + za * mean(za * u.abs()))
+        td, tda = w * zd + uw * z + ub, w.abs() * zda + uw.abs() * za + ub.abs()
+        q, qa = m * g * d2 * td, m * g.abs() * ((2 + ta) if on else 0.0) * tda
+        add = lambda v: v.expand(x.shape).sum(dim=(0, 3)).reshape(-1)
+        for k, v in (("gw", h * z), ("gw_", ha * za), ("dw", q * z + h * zd), ("dw_", qa * za + ha * zda)):
+            out[k].append(add(v))
+        if scalar:
+            for k, v in (("gb", h), ("gb_", ha), ("db", q), ("db_", qa)):
+                out[k].append(add(v))
+        ch, sc, col = ch + ir.mul, sc + (ir.mul if scalar else 0), col + ir.mul * d
+    return {k: torch.cat(v) for k, v in out.items()}
+
+
+@pytest.mark.parametrize("irreps,groups", [("64x0e+64x1o+64x2e", 8), ("40x0e+40x1o", 4), ("25x0e+7x0o+11x1o+5x2e", 1)])
+@pytest.mark.parametrize("act,p", [(None, 0.0), ("silu", 0.2)])
+def test_parameter_gradients_of_many_segments(e3b, irreps, groups, act, p):
+    """More segments than blocks, and tiles with different numbers of blocks: every block's column sums have to come
+    in.  96 half steps of the terms' absolute values for the first derivative (64 rows of a thread in float32, at most
+    32 pointwise roundings), 288 for the second (four columns to a thread's group sums).  One block's share, some 27
+    of 8000 rows, has a signed sum of about 5 in 6400: 8e-4, against 6e-6 and 1.7e-5."""
+    counts = [1 + i % 7 for i in range(2000)]
+    N = sum(counts)
+    f = e3b.Features(irreps, groups=groups)
+    seg = e3b.Segments.from_counts(counts)
+    gen = torch.Generator(DEV).manual_seed(5)
+    t = {k: torch.randn(*s, device=DEV, generator=gen) for k, s in
+         (("x", (N, f.dim)), ("g", (N, f.dim)), ("ux", (N, f.dim)), ("w", (f.n_channels,)), ("b", (f.n_scalars,)),
+          ("uw", (f.n_channels,)), ("ub", (f.n_scalars,)))}
+    kw = dict(segments=seg, act=act, p=p, rng=(3, 1) if p else None)
+    _, st = e3b.group_norm_forward(f, t["x"], t["w"], t["b"], **kw)
+    got = dict(zip(("gw", "gb"), e3b.group_norm_backward(f, t["x"], st, t["g"], t["w"], t["b"], **kw)[1:]))
+    got.update(zip(("dw", "db"), e3b.group_norm_double_backward(f, t["x"], st, t["g"], t["w"], t["b"], t["ux"], t["uw"],
+                                                                t["ub"], **kw)[2:]))
+    wide = e3b.Features(irreps, dtype=torch.float64)
+    factor = torch.ones(N, f.dim, device=DEV, dtype=torch.float64)
+    if p:
+        factor = e3b.dropout_forward(wide, factor, p, (3, 1))
+    ref = _gradient_sizes(irreps, groups, counts, {k: v.double() for k, v in t.items()}, act, factor)
+    for k, steps in (("gw", 96), ("gb", 96), ("dw", 288), ("db", 288)):
+        worst = float(((got[k].double() - ref[k]).abs() / (steps * 2.0 ** -24 * ref[k + "_"] + 1e-30)).max())
+        assert worst <= 1, (k, worst)
+    e3b.device_status()
+
+
+@pytest.mark.parametrize("rows", [1, 25])
+def test_short_segments_beyond_32_bit_offsets(e3b, rows):
+    """1.1 M rows of 2048 columns (2.25e9 values) in one-row segments and in segments of 25 rows: the kernels that
+    hold a segment in one block, all three forms.  The last segments against the oracle."""
+    irreps, N, last = "128x0e+128x1o+128x2e+128x3o", 1_100_000, 25
+    f = e3b.Features(irreps, groups=16)
+    seg = e3b.Segments(torch.arange(0, N + 1, rows, dtype=torch.int32, device=DEV), N, max_rows=rows)
+
+    def fill(seed):
+        t = torch.empty(N, f.dim, device=DEV)
+        for a in range(0, N, 100_000):
+            t[a:a + 100_000].normal_(generator=torch.Generator(DEV).manual_seed(a + seed))
+        return t
+
+    x, g, u = fill(0), fill(1), fill(2)
+    xn, gn, un = (t[N - last:].cpu().numpy() for t in (x, g, u))
+    ptr = np.arange(0, last + 1, rows)
+    kw = dict(segments=seg, act="silu", p=0.5, rng=(3, 1))
+    okw = dict(act="silu", factor=oracle.dropout_factor(irreps, last, 0.5, 3, 1, row0=N - last), scale=True)
+    y, st = e3b.group_norm_forward(f, x, **kw)
+    _close(y[N - last:], *oracle.group_norm(irreps, 16, ptr, xn, **okw), 96, torch.float32, "y")
+    del y
+    gx, _, _ = e3b.group_norm_backward(f, x, st, g, **kw)
+    ref = oracle.group_norm_backward(irreps, 16, ptr, xn, gn, **okw)
+    _close(gx[N - last:], ref[0], ref[3], 96, torch.float32, "gx")
+    del gx
+    dg, dx, _, _ = e3b.group_norm_double_backward(f, x, st, g, u_x=u, **kw)
+    ref = oracle.group_norm_double_backward(irreps, 16, ptr, xn, gn, u_x=un, **okw)
+    for i, (got, what) in enumerate(((dg, "dg"), (dx, "dx"))):
+        _close(got[N - last:], ref[i], ref[i + 4], 288, torch.float32, what)
+    e3b.device_status()
+    del x, g, u, st, dg, dx
+    torch.cuda.empty_cache()
