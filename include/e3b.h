@@ -395,9 +395,11 @@ typedef enum { E3_ACT_NONE = 0, E3_ACT_SILU = 1 } e3_act;
  * Sums run in the rows' type over at most 64 rows of a thread and over the threads, CTAs and chunks of a
  * segment (means relative to a value of the segment, and kept in double).  Their order is fixed: results
  * are bitwise repeatable.  The kernels of long segments, and of the parameters' gradients where no cluster
- * of blocks shares a segment, are cooperative launches; all calls can be recorded into a CUDA graph (after a first call on the device,
- * which sets up its status word).  N <= 2^31 - 65536, 1 <= B < 2^31.  N == 0 leaves every row output alone and
- * zero-fills the parameters' gradients. */
+ * of blocks shares a segment, are cooperative launches; all calls can be recorded into a CUDA graph (after
+ * a first call on the device, which sets up its status word).  N <= 2^31 - 65536, 1 <= B < 2^31.  N == 0
+ * leaves every row output alone and zero-fills the parameters' gradients.
+ * A segment's rows have to be in one call: on rows that are spread over several devices the statistics are
+ * those of the rows at hand (the dropout's row0 places its mask, nothing else). */
 E3_API e3_status e3_group_norm_workspace_size(const e3_features* features, int64_t N, int64_t B, int64_t max_rows,
                                               size_t* bytes);
 E3_API e3_status e3_group_norm_forward(const e3_features* features, int64_t N, int64_t B, const int32_t* row_ptr,

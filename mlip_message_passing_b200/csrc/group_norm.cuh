@@ -20,8 +20,10 @@
 //          tiles, meet, join them, meet, and read their rows again.
 // Measured (B200, float32, one call): local, 24000 one-row segments of 2048 columns, forward 97 us = 4.1 TB/s
 // (62% of a copy): two CTAs of 512 threads, bound by the chain from barrier to barrier; 512 segments of 34 rows x
-// 512 columns with dropout, forward 29 us and backward 51 us.  Grid, one segment of 24000 x 2048: forward 107 us
-// (590 MB in three passes, 5.5 TB/s), backward 190 us with dropout (983 MB, 5.2 TB/s).
+// 512 columns with dropout, forward 29 us and backward 51 us.  Grid, one segment of 24000 x 2048: forward 108 us
+// (590 MB in three passes), backward 190 us with dropout (983 MB in five).  L2 serves a part of the second reads: with
+// dropout 494 and 909 MB pass DRAM, 50 and 60 % of its rate under ncu, so the forward is bound by the latency of
+// memory (20 warps an SM), the backward by its instructions (16), and neither by DRAM.
 // Tried for the grid kernel and dropped: slabs of columns small enough for L2, one after another (24, 50, 100 MB:
 // forward 197, 152, 136 us; a meeting and a join per slab, and narrow tiles, cost more than the re-read; L2 also keeps
 // only about 60 MB of what one pass read for the next); rows through registers instead of cp.async; sharing the

@@ -50,7 +50,7 @@ template <typename K>
 int gn_resident(K kernel, size_t smem, std::atomic<int64_t>* cache, bool cluster, int threads = GN_THREADS) {
   int dev = 0;
   cudaGetDevice(&dev);
-  // the cache holds the answer for the last size asked for (sizes differ by a few hundred bytes at most)
+  // the cache holds the answer for the last size asked for; layouts that take turns ask again at each call
   const int64_t hit = dev < 64 ? cache[dev].load(std::memory_order_relaxed) : 0;
   int n = hit >> 32 == int64_t(smem) ? int(hit & 0xFFFFFFFF) : 0;
   if (n == 0) {

@@ -858,7 +858,8 @@ def group_norm_forward(features, x, weight=None, bias=None, segments=None, eps=1
                        row0=0, out=None):
     """(y, stats): group norm of rows x [N, dim] over the segments (None: one segment of all rows), then
     the activation on the 0e channels, then dropout (e3_group_norm_forward).  ``stats`` [B, n_groups, 2]
-    float64 holds (mean, 1 / deviation) for the backward.  Padding rows of y are zero."""
+    float64 holds (mean, 1 / deviation) for the backward.  Padding rows of y are zero.  ``row0`` is for the dropout
+    alone: a structure's statistics need all of its rows in one call."""
     N, B, row_ptr, max_rows, px, pw, pb = _norm_args(features, x, weight, bias, segments, act)
     if out is None:
         out = torch.empty_like(x)
