@@ -242,6 +242,14 @@ struct GnSlots {
   }
 };
 
+// A product that is rounded by itself, never fused into a sum.  The double backward takes differences of sums that
+// cancel altogether in a group of one even scalar (z = 0, so nothing depends on x there, while r is up to
+// eps^(-1/2)): both sides have to round alike.
+__device__ __forceinline__ float gn_mul(float a, float b) { return __fmul_rn(a, b); }
+__device__ __forceinline__ double gn_mul(double a, double b) { return __dmul_rn(a, b); }
+__device__ __forceinline__ float gn_fma(float a, float b, float c) { return __fmaf_rn(a, b, c); }
+__device__ __forceinline__ double gn_fma(double a, double b, double c) { return __fma_rn(a, b, c); }
+
 // h, q's factor m g a''(t), m a'(t) and z of one value
 template <typename T>
 struct GnSecond {
@@ -322,7 +330,7 @@ struct GnAcc<T, VEC, GN_DBL, DROP> {
     for (int i = 0; i < VEC; ++i) {
       const GnSecond<T> e = gn_second<KIND, T, VEC, DROP>(c, st, kp, i, v.x.v[i], v.g.v[i]);
       const T ux = v.u.v[i], cc = c.w[i] * e.h;
-      T q = c.uw[i] * e.h;
+      T q = gn_mul(c.uw[i], e.h);
       s[1] += e.z * ux;
       s[3] += cc * e.z;
       s[4] += cc * ux;
@@ -332,7 +340,7 @@ struct GnAcc<T, VEC, GN_DBL, DROP> {
       }
       if (KIND == GN_ACT) {
         const T wq = c.w[i] * c.w[i] * e.q1;
-        q += c.w[i] * e.q1 * (c.uw[i] * e.z + c.ub[i]);
+        q = gn_fma(c.w[i], gn_mul(e.q1, gn_fma(c.uw[i], e.z, c.ub[i])), q);
         s[5] += wq;
         s[6] += wq * e.z;
         s[7] += wq * e.z * e.z;
@@ -373,7 +381,7 @@ __device__ __forceinline__ void gn_finish(const T* s, T n, bool scalar, T r, T e
     o[0] = m1;
     o[1] = m2;
     o[2] = mcz;
-    o[3] = scalar ? in * (r * (s[8] - m1 * s[5] - m2 * s[6]) + s[10] - r * m2 * s[2] - r * mcz * s[0]) : T(0);
+    o[3] = scalar ? in * (r * (s[8] - gn_mul(m1, s[5]) - m2 * s[6]) + s[10] - r * m2 * s[2] - r * mcz * s[0]) : T(0);
     o[4] = in * (r * (s[9] - m1 * s[6] - m2 * s[7]) + s[11] - r * m2 * s[3] - r * mcz * s[1]);
     o[5] = in * (r * (s[4] - m1 * s[2] - m2 * s[3]));
   }
@@ -414,9 +422,9 @@ __device__ __forceinline__ void gn_apply(const NormArgs& a, const GnCol<T, VEC, 
       const GnSecond<T> e = gn_second<KIND, T, VEC, DROP>(c, st, kp, i, v.x.v[i], v.g.v[i]);
       const T ux = v.u.v[i], cc = c.w[i] * e.h;
       const T zd = st.r * (ux - k[0] - e.z * k[1]);
-      const T td = c.w[i] * zd + c.uw[i] * e.z + c.ub[i];
-      const T q = KIND == GN_ACT ? e.q1 * td : T(0);
-      const T C = c.w[i] * q + c.uw[i] * e.h - st.r * (k[1] * cc + k[2] * ux);
+      const T td = gn_fma(c.w[i], zd, gn_fma(c.uw[i], e.z, c.ub[i]));
+      const T q = KIND == GN_ACT ? gn_mul(e.q1, td) : T(0);
+      const T C = gn_fma(c.w[i], q, gn_mul(c.uw[i], e.h)) - st.r * (k[1] * cc + k[2] * ux);
       dg.v[i] = e.d1 * td;
       o.v[i] = st.r * (C - k[3] - e.z * (k[4] + k[5]));
       cw[i] += q * e.z + e.h * zd;

@@ -398,3 +398,33 @@ def test_short_segments_beyond_32_bit_offsets(e3b, rows):
     e3b.device_status()
     del x, g, u, st, dg, dx
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float64])
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("hint", ["max", 0])
+def test_groups_of_one_scalar_have_no_gradient(e3b, dtype, act, hint):
+    """One-row segments, one 0e channel to a group: z = 0 whatever x is, so the first derivative is 0 and the second
+    has none with respect to x, exactly, although r = 316 multiplies what is left of differences there.  The other
+    columns are those of the oracle."""
+    irreps, groups, n = "4x0e+8x1o+4x0e", 4, 300
+    f, seg = e3b.Features(irreps, groups=groups, dtype=dtype), e3b.Segments.from_counts([1] * n)
+    if hint != "max":
+        seg.max_rows = hint
+    gen = torch.Generator(DEV).manual_seed(7)
+    x, g, u = (torch.randn(n, f.dim, device=DEV, dtype=dtype, generator=gen) for _ in range(3))
+    w, b, uw, ub = (torch.randn(k, device=DEV, dtype=dtype, generator=gen) for k in (f.n_channels, f.n_scalars) * 2)
+    kw = dict(segments=seg, act=act)
+    y, st = e3b.group_norm_forward(f, x, w, b, **kw)
+    gx, _, _ = e3b.group_norm_backward(f, x, st, g, w, b, **kw)
+    scalar = torch.ones(f.dim, dtype=torch.bool, device=DEV)
+    scalar[4:28] = False
+    assert not bool(gx[:, scalar].any())
+    for ups in (dict(u_x=u), dict(u_x=u, u_weight=uw, u_bias=ub), dict(u_weight=uw, u_bias=ub)):
+        dg, dx, _, _ = e3b.group_norm_double_backward(f, x, st, g, w, b, **ups, **kw)
+        assert not bool(dx[:, scalar].any())
+        ref = oracle.group_norm_double_backward(irreps, groups, np.arange(n + 1), *(t.cpu().numpy() for t in (x, g, w, b)),
+                                                act=act, scale=True, **{k: t.cpu().numpy() for k, t in ups.items()})
+        _close(dg, ref[0], ref[4], 288, dtype, "dg")
+        _close(dx, ref[1], ref[5], 288, dtype, "dx")
+    e3b.device_status()
