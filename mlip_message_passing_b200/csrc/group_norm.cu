@@ -111,7 +111,7 @@ GnConfig configure(const e3_features* f, int64_t N, int64_t B, int64_t max_rows,
     c.local = c.one_row = true;
     t = &f->rows;
     a->cap = a->k = 1;
-    a->j = std::min(GN_ROW_THREADS / t->tx, GN_ROW_ITEMS / (gn_reg_segments(op, f->vec) * t->groups));
+    a->j = std::min(GN_ROW_THREADS / t->tx, std::max(1, GN_ROW_ITEMS / (gn_reg_segments(op, f->vec) * t->groups)));
   } else if (t->n() > 0 && t->n() <= GN_LOCAL_TILES && (held || turns)) {
     c.local = true;
     a->cap = held ? RP : GN_FLUSH;
@@ -243,9 +243,11 @@ void make_tiles(e3_features* f) {
   for (int i = 0; i < 9; ++i)
     if ((f->wide << i) <= GN_THREADS)
       f->local[i] = best_tiles(L, f->vec, f->wide, GN_THREADS >> i, 1 << i, GN_THREADS);
-  if (f->wide <= GN_ROW_THREADS)
-    f->rows = best_tiles(L, f->vec, f->wide, GN_ROW_THREADS, 1, GN_ROW_THREADS,
-                         GN_ROW_ITEMS / gn_reg_segments(GN_FWD, f->vec));
+  if (f->wide <= GN_ROW_THREADS) {
+    // doubles: no more groups to a tile than a batch of one segment a thread has coefficients for
+    const int most = f->dtype == E3_F64 ? GN_ROW_ITEMS / gn_reg_segments(GN_FWD, f->vec) : GN_ROW_THREADS;
+    f->rows = best_tiles(L, f->vec, f->wide, GN_ROW_THREADS, 1, GN_ROW_THREADS, most);
+  }
   f->grid = equal_tiles(L, f->vec);
   // narrow tiles for clusters, which leave the CTAs more row lanes
   if (f->wide <= 64) f->narrow = cut_tiles(L, f->vec, std::max(f->wide, 8));

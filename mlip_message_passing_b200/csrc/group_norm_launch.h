@@ -12,8 +12,9 @@ static_assert(sizeof(NormArgs) <= 4096, "kernel arguments");
 // Threads of a CTA of the local kernel when every segment is one row: rows are wide, batches short (256 threads
 // leave a third of them idle on 2048 columns with one group per block).
 constexpr int GN_ROW_THREADS = 512;
-// (Segment, group) pairs of a batch of one-row segments at most: 8 segments a thread of one-element vectors of
-// doubles take 160 KB for rows and sums, and 24 bytes a pair for the forward's coefficients.
+// (Segment, group) pairs of a batch of one-row segments at most (twice as many for floats, whose tiles may have 512
+// groups of one column): 8 segments a thread of one-element vectors of doubles take 160 KB for rows and sums, and 24
+// bytes a pair for the forward's coefficients.
 constexpr int GN_ROW_ITEMS = 2048;
 
 struct GnConfig {

@@ -428,3 +428,19 @@ def test_groups_of_one_scalar_have_no_gradient(e3b, dtype, act, hint):
         _close(dg, ref[0], ref[4], 288, dtype, "dg")
         _close(dx, ref[1], ref[5], 288, dtype, "dx")
     e3b.device_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float64])
+def test_one_row_segments_of_the_most_groups(e3b, dtype):
+    """32768 one-column groups, the most that a row can have: 64 tiles of 512 for floats, more for doubles, which leave
+    them to the kernel for long segments.  y = x / sqrt(x^2 + eps): at most 8 roundings, the root's step included."""
+    f = e3b.Features("32768x0o", groups=32768, dtype=dtype)
+    x = torch.randn(40, f.dim, device=DEV, dtype=dtype, generator=torch.Generator(DEV).manual_seed(2))
+    y, st = e3b.group_norm_forward(f, x, segments=e3b.Segments.from_counts([1] * 40))
+    want = x.double() / torch.sqrt(x.double() ** 2 + 1e-5)
+    half = 2.0 ** -24 if dtype is torch.float32 else 2.0 ** -53
+    assert float(((y.double() - want).abs() / want.abs()).max()) <= 8 * half
+    gx, _, _ = e3b.group_norm_backward(f, x, st, x, segments=e3b.Segments.from_counts([1] * 40))
+    # grad_x = r (c - z (c z)) with c = x, in terms of r x = y: y (1 - y^2); the difference cancels, so against y
+    assert float(((gx.double() - want * (1 - want ** 2)).abs() / want.abs()).max()) <= 16 * half
+    e3b.device_status()
